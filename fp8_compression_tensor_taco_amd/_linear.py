@@ -1,0 +1,304 @@
+"""ctypes binding over the 8-bit linear layer's C ABI (include/taco_linear.h).
+
+Argument marshalling only, as in _binding: the operators run in the HIP kernels
+of libtaco.so, there is no CPU fallback, and outputs may be passed in to avoid
+allocation.  Matrices are 2-D; an input that is not contiguous is copied.
+
+Codes and scales are uint8 tensors.  ``q.view(torch.float8_e4m3fn)`` and
+``scale.view(torch.float8_e8m0fnu)`` give their values.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._binding import _check, _on, _stream, _workspace, load
+
+BLOCK = 128
+
+_vp = ctypes.c_void_p
+_i64 = ctypes.c_int64
+_size = ctypes.c_size_t
+_SIGNATURES = {
+    "taco_fp8_cols": (_i64, [_i64]),
+    "taco_fp8_scale_cols": (_i64, [_i64]),
+    "taco_quantize_rows": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+    "taco_quantize_weight": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "taco_rmsnorm_quantize": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, ctypes.c_float, _vp, _vp, _vp, _vp, _vp]),
+    "taco_rmsnorm_backward_workspace_bytes": (_size, [_i64, _i64]),
+    "taco_rmsnorm_backward": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _size, _vp]),
+    "taco_matmul_fp8_workspace_bytes": (_size, [_i64, _i64, _i64]),
+    "taco_matmul_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _size, _vp]),
+    "taco_wgrad_fp8_workspace_bytes": (_size, [_i64, _i64, _i64]),
+    "taco_wgrad_fp8": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, ctypes.c_int32, _vp, _size, _vp]),
+    "taco_swiglu_quantize": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "taco_swiglu_backward": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
+}
+_typed = None
+
+
+def _lib():
+    global _typed
+    if _typed is None:
+        lib = load()
+        for name, (restype, argtypes) in _SIGNATURES.items():
+            f = getattr(lib, name)
+            f.restype, f.argtypes = restype, argtypes
+        _typed = lib
+    return _typed
+
+
+def fp8_cols(cols: int) -> int:
+    """Codes in a row of ``cols`` columns: rounded up to whole blocks of 128."""
+    if cols < 1:
+        raise ValueError("cols must be at least 1")
+    return -(-cols // BLOCK) * BLOCK
+
+
+def fp8_scale_cols(cols: int) -> int:
+    """Scale bytes in a row of ``cols`` columns: one per 128, rounded up to 4."""
+    return -(-fp8_cols(cols) // (4 * BLOCK)) * 4
+
+
+def _input(t, name, dtype, shape=None, dims=2):
+    """The tensor as the kernels take it: on a GPU, contiguous, 16-byte aligned."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("libtaco works on GPU tensors only (no CPU fallback)")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _output(t, name, dtype, shape, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+    return t
+
+
+def _same_device(*tensors):
+    for t in tensors[1:]:
+        if t is not None and t.device != tensors[0].device:
+            raise ValueError("all tensors must be on the same device")
+    return tensors[0].device
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(device, nbytes, kind, handle):
+    """(pointer, bytes) of the binding's workspace; none where 0 bytes are needed."""
+    if nbytes == 0:
+        return None, 0
+    ws = _workspace(device, nbytes, kind, handle)
+    return ws.data_ptr(), ws.numel()
+
+
+def quantize_rows(x: torch.Tensor, *, q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
+    """Quantise bf16 [rows, cols] into the block format.
+
+    Returns (q uint8 [rows, fp8_cols(cols)], scale uint8 [rows, fp8_scale_cols(cols)])."""
+    with _on(stream):
+        x = _input(x, "x", torch.bfloat16)
+        rows, cols = x.shape
+        dev = x.device
+        q = _output(q, "q", torch.uint8, (rows, fp8_cols(cols)), dev)
+        scale = _output(scale, "scale", torch.uint8, (rows, fp8_scale_cols(cols)), dev)
+        _check(_lib().taco_quantize_rows(x.data_ptr(), rows, cols, q.data_ptr(), scale.data_ptr(), _stream(dev, stream)))
+        return q, scale
+
+
+def quantize_weight(w: torch.Tensor, *, transposed: bool = True, q: torch.Tensor | None = None,
+                    scale: torch.Tensor | None = None, qt: torch.Tensor | None = None,
+                    scale_t: torch.Tensor | None = None, stream=None):
+    """Quantise a bf16 weight [rows, cols], one scale per 128 x 128 block.
+
+    Returns (q, scale, qt, scale_t): the weight [rows, cols] and the same codes
+    of its transpose [cols, rows], both in the weight format, for the forward
+    product and the input's gradient.  transposed=False gives None for the last two."""
+    with _on(stream):
+        w = _input(w, "w", torch.bfloat16)
+        rows, cols = w.shape
+        dev = w.device
+        q = _output(q, "q", torch.uint8, (rows, fp8_cols(cols)), dev)
+        scale = _output(scale, "scale", torch.uint8, (fp8_cols(rows) // BLOCK, fp8_scale_cols(cols)), dev)
+        if transposed:
+            qt = _output(qt, "qt", torch.uint8, (cols, fp8_cols(rows)), dev)
+            scale_t = _output(scale_t, "scale_t", torch.uint8, (fp8_cols(cols) // BLOCK, fp8_scale_cols(rows)), dev)
+        elif qt is not None or scale_t is not None:
+            raise ValueError("qt and scale_t are outputs of transposed=True")
+        _check(_lib().taco_quantize_weight(w.data_ptr(), rows, cols, q.data_ptr(), scale.data_ptr(), _ptr(qt),
+                                           _ptr(scale_t), _stream(dev, stream)))
+        return q, scale, qt, scale_t
+
+
+def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, *,
+                     residual: torch.Tensor | None = None, z: torch.Tensor | None = None,
+                     rstd: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                     scale: torch.Tensor | None = None, stream=None):
+    """Root-mean-square norm of bf16 x (+ residual), quantised.
+
+    Returns (z, rstd, q, scale): z = bf16(x + residual), the new residual
+    stream (x itself without a residual); rstd fp32 [tokens]; and
+    z * rstd * weight in the block format."""
+    with _on(stream):
+        x = _input(x, "x", torch.bfloat16)
+        tokens, hidden = x.shape
+        weight = _input(weight, "weight", torch.bfloat16, (hidden,), 1)
+        dev = _same_device(x, weight, residual)
+        if residual is not None:
+            residual = _input(residual, "residual", torch.bfloat16, (tokens, hidden))
+            z = _output(z, "z", torch.bfloat16, (tokens, hidden), dev)
+        elif z is not None:
+            raise ValueError("z is an output of the call with a residual")
+        rstd = _output(rstd, "rstd", torch.float32, (tokens,), dev)
+        q = _output(q, "q", torch.uint8, (tokens, fp8_cols(hidden)), dev)
+        scale = _output(scale, "scale", torch.uint8, (tokens, fp8_scale_cols(hidden)), dev)
+        _check(_lib().taco_rmsnorm_quantize(x.data_ptr(), _ptr(residual), weight.data_ptr(), tokens, hidden, eps,
+                                            _ptr(z), rstd.data_ptr(), q.data_ptr(), scale.data_ptr(),
+                                            _stream(dev, stream)))
+        return x if z is None else z, rstd, q, scale
+
+
+def rmsnorm_backward(dy: torch.Tensor, z: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, *,
+                     dz: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                     dweight: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradient of rmsnorm_quantize for dy, the gradient of its (unquantised) output.
+
+    dz is the gradient that reached z by the residual path.  Returns (dx bf16,
+    the gradient of x and of the residual; dweight fp32 [hidden])."""
+    with _on(stream):
+        dy = _input(dy, "dy", torch.bfloat16)
+        tokens, hidden = dy.shape
+        z = _input(z, "z", torch.bfloat16, (tokens, hidden))
+        rstd = _input(rstd, "rstd", torch.float32, (tokens,), 1)
+        weight = _input(weight, "weight", torch.bfloat16, (hidden,), 1)
+        if dz is not None:
+            dz = _input(dz, "dz", torch.bfloat16, (tokens, hidden))
+        dev = _same_device(dy, z, rstd, weight, dz, workspace)
+        dx = _output(dx, "dx", torch.bfloat16, (tokens, hidden), dev)
+        dweight = _output(dweight, "dweight", torch.float32, (hidden,), dev)
+        lib, handle = _lib(), _stream(dev, stream)
+        if workspace is None:
+            ws = _scratch(dev, lib.taco_rmsnorm_backward_workspace_bytes(tokens, hidden), "rmsnorm_backward", handle)
+        else:
+            ws = _given(workspace)
+        _check(lib.taco_rmsnorm_backward(dy.data_ptr(), z.data_ptr(), rstd.data_ptr(), weight.data_ptr(), _ptr(dz),
+                                         tokens, hidden, dx.data_ptr(), dweight.data_ptr(), *ws, handle))
+        return dx, dweight
+
+
+def _given(workspace):
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def matmul_fp8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Tensor, *,
+               out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """bf16 [m, n] = a b^T of a [m, k] in the block format and b [n, k] in the weight format.
+
+    With a = x and b = w a linear layer's output; with a = dy and b the
+    transposed weight, the gradient of its input."""
+    with _on(stream):
+        qa, qb = _input(qa, "qa", torch.uint8), _input(qb, "qb", torch.uint8)
+        (m, k), n = qa.shape, qb.shape[0]
+        if k == 0 or k % BLOCK or qb.shape[1] != k:
+            raise ValueError(f"qa and qb must have the same number of columns, a multiple of {BLOCK}: "
+                             f"got {k} and {qb.shape[1]}")
+        sa = _input(sa, "sa", torch.uint8, (m, fp8_scale_cols(k)))
+        sb = _input(sb, "sb", torch.uint8, (-(-n // BLOCK), fp8_scale_cols(k)))
+        dev = _same_device(qa, sa, qb, sb, workspace)
+        out = _output(out, "out", torch.bfloat16, (m, n), dev)
+        lib, handle = _lib(), _stream(dev, stream)
+        if workspace is None:
+            ws = _scratch(dev, lib.taco_matmul_fp8_workspace_bytes(m, n, k), "matmul_fp8", handle)
+        else:
+            ws = _given(workspace)
+        _check(lib.taco_matmul_fp8(qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), m, n, k,
+                                   out.data_ptr(), *ws, handle))
+        return out
+
+
+def wgrad_fp8(dy: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, cols: int, *, dw: torch.Tensor | None = None,
+              accumulate: bool = False, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """fp32 [n, cols] = dy^T x of bf16 dy [tokens, n] and x [tokens, cols] in the block format.
+
+    x is a linear layer's input as it was kept in 8 bits.  accumulate=True adds
+    to dw, which must then be given."""
+    with _on(stream):
+        dy = _input(dy, "dy", torch.bfloat16)
+        tokens, n = dy.shape
+        q = _input(q, "q", torch.uint8, (tokens, fp8_cols(cols)))
+        scale = _input(scale, "scale", torch.uint8, (tokens, fp8_scale_cols(cols)))
+        if accumulate and dw is None:
+            raise ValueError("accumulate=True adds to dw: pass it")
+        dev = _same_device(dy, q, scale, workspace)
+        dw = _output(dw, "dw", torch.float32, (n, cols), dev)
+        lib, handle = _lib(), _stream(dev, stream)
+        if workspace is None:
+            ws = _scratch(dev, lib.taco_wgrad_fp8_workspace_bytes(tokens, n, cols), "wgrad_fp8", handle)
+        else:
+            ws = _given(workspace)
+        _check(lib.taco_wgrad_fp8(dy.data_ptr(), q.data_ptr(), scale.data_ptr(), tokens, n, cols, dw.data_ptr(),
+                                  int(bool(accumulate)), *ws, handle))
+        return dw
+
+
+def swiglu_quantize(gu: torch.Tensor, *, checkpoint: bool = True, hq: torch.Tensor | None = None,
+                    hs: torch.Tensor | None = None, cq: torch.Tensor | None = None, cs: torch.Tensor | None = None,
+                    stream=None):
+    """SiLU-gated unit of bf16 gu [tokens, 2 * inner] (gate, then up), quantised.
+
+    Returns (hq, hs, cq, cs): silu(gate) * up in the block format, and gate and
+    up in 8 bits for swiglu_backward (checkpoint=False gives None for those)."""
+    with _on(stream):
+        gu = _input(gu, "gu", torch.bfloat16)
+        tokens, both = gu.shape
+        if both == 0 or both % 2:
+            raise ValueError("gu must have an even number of columns: gate, then up")
+        inner = both // 2
+        dev, wide = gu.device, fp8_cols(inner)
+        hq = _output(hq, "hq", torch.uint8, (tokens, wide), dev)
+        hs = _output(hs, "hs", torch.uint8, (tokens, fp8_scale_cols(inner)), dev)
+        if checkpoint:
+            cq = _output(cq, "cq", torch.uint8, (tokens, 2 * wide), dev)
+            cs = _output(cs, "cs", torch.uint8, (tokens, fp8_scale_cols(2 * wide)), dev)
+        elif cq is not None or cs is not None:
+            raise ValueError("cq and cs are outputs of checkpoint=True")
+        _check(_lib().taco_swiglu_quantize(gu.data_ptr(), tokens, inner, hq.data_ptr(), hs.data_ptr(), _ptr(cq),
+                                           _ptr(cs), _stream(dev, stream)))
+        return hq, hs, cq, cs
+
+
+def swiglu_backward(dh: torch.Tensor, cq: torch.Tensor, cs: torch.Tensor, *, quantize: bool = True,
+                    dgu: torch.Tensor | None = None, dq: torch.Tensor | None = None, ds: torch.Tensor | None = None,
+                    stream=None):
+    """Gradient of swiglu_quantize for dh bf16 [tokens, inner], at the checkpoint's gate and up.
+
+    Returns (dgu bf16 [tokens, 2 * inner], dq, ds): the gradient of gu, and the
+    same in the block format (quantize=False gives None for those)."""
+    with _on(stream):
+        dh = _input(dh, "dh", torch.bfloat16)
+        tokens, inner = dh.shape
+        wide = fp8_cols(inner)
+        cq = _input(cq, "cq", torch.uint8, (tokens, 2 * wide))
+        cs = _input(cs, "cs", torch.uint8, (tokens, fp8_scale_cols(2 * wide)))
+        dev = _same_device(dh, cq, cs)
+        dgu = _output(dgu, "dgu", torch.bfloat16, (tokens, 2 * inner), dev)
+        if quantize:
+            dq = _output(dq, "dq", torch.uint8, (tokens, fp8_cols(2 * inner)), dev)
+            ds = _output(ds, "ds", torch.uint8, (tokens, fp8_scale_cols(2 * inner)), dev)
+        elif dq is not None or ds is not None:
+            raise ValueError("dq and ds are outputs of quantize=True")
+        _check(_lib().taco_swiglu_backward(dh.data_ptr(), cq.data_ptr(), cs.data_ptr(), tokens, inner,
+                                           dgu.data_ptr(), _ptr(dq), _ptr(ds), _stream(dev, stream)))
+        return dgu, dq, ds

@@ -15,7 +15,9 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libtaco.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-SOURCES = [os.path.join(CSRC, "taco.hip")]
+SOURCES = [os.path.join(CSRC, "taco.hip")]                  # the compression calls (include/taco.h)
+LINEAR_SOURCES = [os.path.join(CSRC, "rowops.hip"),         # the 8-bit linear layer (include/taco_linear.h)
+                  os.path.join(CSRC, "matmul.hip")]
 ARCH = "gfx950"
 
 
@@ -44,7 +46,7 @@ def compile_flags() -> list[str]:
 def build_library(verbose: bool = True) -> str:
     """Compile every HIP source into ``libtaco.so`` next to this file; returns its path."""
     tmp = LIB_PATH + ".tmp"
-    cmd = [hipcc(), *compile_flags(), "-shared", *SOURCES, "-o", tmp]
+    cmd = [hipcc(), *compile_flags(), "-shared", "-parallel-jobs=3", *SOURCES, *LINEAR_SOURCES, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,0 +1,167 @@
+/*
+ * libtaco -- operators of an 8-bit linear layer for AMD Instinct MI355X
+ * (gfx950): block-scaled FP8 quantisation, a root-mean-square norm with a
+ * residual and a quantised output, the FP8 matrix product, the weight gradient
+ * from an 8-bit checkpoint of the layer's input, and a SiLU-gated unit that
+ * keeps its input in 8 bits.  Part of libtaco.so beside the compression calls
+ * of taco.h, whose conventions hold here too.
+ *
+ * Block format.  A matrix of `rows` rows and `cols` columns is held as
+ *   q      uint8 [rows, taco_fp8_cols(cols)]: OCP FP8 E4M3FN codes; the columns
+ *          from `cols` up to the next multiple of 128 hold code 0.
+ *   scale  uint8 [rows, taco_fp8_scale_cols(cols)]: one E8M0 byte e for each 128
+ *          consecutive columns of a row, standing for 2^(e - 127); the row is
+ *          padded with 127 to a multiple of four bytes.
+ * An element's value is decode(q) * 2^(e - 127).  A block's scale is the
+ * smallest power of two (2^-126 at least) that brings its largest magnitude to
+ * 448 or less, and 1 for a block of zeros; the division by it is exact, and the
+ * code is the nearest E4M3 value, ties to even, so nothing saturates.  A block
+ * that holds an infinity or a NaN has scale byte 255 (NaN) and codes 0x7F in
+ * all 128 columns: it reads as NaN throughout, in every call that takes it.
+ * A weight has one scale for each 128 x 128 block instead: scale is uint8
+ * [ceil(rows / 128), taco_fp8_scale_cols(cols)].
+ * Scale bytes given to a call may be any of 0..255, codes any value.
+ *
+ * Shapes.  Any 1 <= rows <= 2^24 and 1 <= cols <= 2^22 with rows * padded cols
+ * <= 2^34; nothing needs to be a multiple of anything.  Other limits are named
+ * at the calls.
+ *
+ * Pointers.  DEVICE pointers, owned by the caller; matrices are row-major and
+ * contiguous.  bf16 and code buffers and dw are 16-byte aligned, other fp32
+ * and scale buffers 4-byte, workspaces 256-byte.  A workspace needs no zero-fill and may
+ * be used by one call at a time.  Calls enqueue work on `stream` and return.
+ * Arguments are checked on the host before any launch: TACO_ERR_NULL,
+ * TACO_ERR_SHAPE, TACO_ERR_ALIGN, TACO_ERR_WORKSPACE, TACO_ERR_ALIAS (an output
+ * overlaps an input or another output), and TACO_ERR_HIP for a failed launch.
+ *
+ * Results are deterministic: no atomics, every sum in one fixed order for a
+ * given shape.
+ */
+#ifndef TACO_LINEAR_H
+#define TACO_LINEAR_H
+
+#include "taco.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Codes per row (cols rounded up to 128) and scale bytes per row (one for each
+ * 128 columns, rounded up to 4) of the block format; -1 for cols < 1. */
+int64_t taco_fp8_cols(int64_t cols);
+int64_t taco_fp8_scale_cols(int64_t cols);
+
+/* Quantise bf16 [rows, cols] into the block format. */
+taco_status_t taco_quantize_rows(const void* x_bf16, int64_t rows, int64_t cols, uint8_t* q,
+                                 uint8_t* scale, taco_stream_t stream);
+
+/*
+ * Quantise a bf16 weight [rows, cols] with one scale for each 128 x 128 block.
+ *   q, scale     out: the weight; scale has ceil(rows / 128) rows
+ *   qt, scale_t  out: the same codes and scales of the transpose, [cols, rows]
+ *                     in the weight format (both NULL: not written)
+ */
+taco_status_t taco_quantize_weight(const void* w_bf16, int64_t rows, int64_t cols, uint8_t* q,
+                                   uint8_t* scale, uint8_t* qt, uint8_t* scale_t,
+                                   taco_stream_t stream);
+
+/*
+ * Root-mean-square norm with the residual's addition and a quantised output:
+ *   z    = bf16(x + residual)                     (x itself without a residual)
+ *   rstd = 1 / sqrt(mean(z^2) + eps)              per row, in fp32
+ *   y    = z * rstd * weight                      in fp32, never stored
+ *   q, scale = y in the block format
+ *   x, residual  bf16 [tokens, hidden]; residual may be NULL
+ *   weight       bf16 [hidden]
+ *   eps          finite and >= 0 (TACO_ERR_SHAPE otherwise); with eps 0 a row
+ *                of zeros gives NaN
+ *   z            out: bf16 [tokens, hidden]; NULL exactly when residual is
+ *   rstd         out: fp32 [tokens]
+ * hidden <= 65536 (TACO_ERR_SHAPE).
+ */
+taco_status_t taco_rmsnorm_quantize(const void* x, const void* residual, const void* weight,
+                                    int64_t tokens, int64_t hidden, float eps, void* z, float* rstd,
+                                    uint8_t* q, uint8_t* scale, taco_stream_t stream);
+
+/*
+ * Gradient of the norm, through y as it was before quantisation: with
+ * xhat = z * rstd and c = mean(dy * weight * xhat) of the row,
+ *   dx      = bf16(rstd * (dy * weight - xhat * c) + dz)
+ *   dweight = sum over tokens of dy * xhat, fp32
+ *   dy         bf16 [tokens, hidden], the gradient of y
+ *   z, rstd    as the forward call wrote them (z = x without a residual)
+ *   dz         bf16 [tokens, hidden], the gradient that reached z itself; may be NULL
+ *   dx         out: bf16 [tokens, hidden], the gradient of x and of the residual
+ *   dweight    out: fp32 [hidden]
+ * hidden <= 65536 (TACO_ERR_SHAPE).
+ */
+size_t taco_rmsnorm_backward_workspace_bytes(int64_t tokens, int64_t hidden);
+taco_status_t taco_rmsnorm_backward(const void* dy, const void* z, const float* rstd,
+                                    const void* weight, const void* dz, int64_t tokens,
+                                    int64_t hidden, void* dx, float* dweight, void* workspace,
+                                    size_t workspace_bytes, taco_stream_t stream);
+
+/*
+ * FP8 matrix product y = a * b^T, bf16:
+ *   qa, sa  a [m, k] in the block format
+ *   qb, sb  b [n, k] in the weight format
+ *   y       out: bf16 [m, n]
+ * Products and sums run on the matrix cores (fp32 accumulators), with the two
+ * blocks' scales applied by the instruction; one rounding to bf16 at the end.
+ * With a = x and b = w it is a layer's output, with a = dy and b = the
+ * transposed weight its input's gradient.
+ * a, b and y within the limits above (TACO_ERR_SHAPE).  The workspace holds partial
+ * sums where k is split over workgroups; it may be NULL where 0 bytes are needed.
+ */
+size_t taco_matmul_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+taco_status_t taco_matmul_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb,
+                              const uint8_t* sb, int64_t m, int64_t n, int64_t k, void* y_bf16,
+                              void* workspace, size_t workspace_bytes, taco_stream_t stream);
+
+/*
+ * Weight gradient of a linear layer whose input was kept in 8 bits:
+ *   dw = dy^T * x  (accumulate 0)   or   dw += dy^T * x  (accumulate 1), fp32
+ *   dy        bf16 [tokens, n]
+ *   q, scale  x [tokens, k] in the block format (the layer's quantised input)
+ *   dw        out: fp32 [n, k]; read first when accumulate is 1
+ * The codes are widened to bf16 on their way into the matrix cores, which is
+ * exact because the scales are powers of two (values below 2^-126 excepted).
+ * dy, x and dw within the limits above (TACO_ERR_SHAPE).
+ */
+size_t taco_wgrad_fp8_workspace_bytes(int64_t tokens, int64_t n, int64_t k);
+taco_status_t taco_wgrad_fp8(const void* dy_bf16, const uint8_t* q, const uint8_t* scale,
+                             int64_t tokens, int64_t n, int64_t k, float* dw, int32_t accumulate,
+                             void* workspace, size_t workspace_bytes, taco_stream_t stream);
+
+/*
+ * SiLU-gated unit with a quantised output and an 8-bit checkpoint of its input:
+ *   h = g * sigmoid(g) * u,  g = gu[:, :inner], u = gu[:, inner:]
+ *   gu      bf16 [tokens, 2 * inner]
+ *   hq, hs  out: h [tokens, inner] in the block format, from g and u as given
+ *   cq, cs  out: the checkpoint, g and u each in the block format side by side:
+ *           cq [tokens, 2 * taco_fp8_cols(inner)], g's padded row, then u's;
+ *           cs [tokens, taco_fp8_scale_cols(2 * taco_fp8_cols(inner))], g's
+ *           bytes, then u's, then the padding.  Both NULL: not kept.
+ */
+taco_status_t taco_swiglu_quantize(const void* gu_bf16, int64_t tokens, int64_t inner, uint8_t* hq,
+                                   uint8_t* hs, uint8_t* cq, uint8_t* cs, taco_stream_t stream);
+
+/*
+ * Gradient of the gated unit at the checkpoint's values of g and u: with
+ * s = sigmoid(g),
+ *   dg = dh * u * s * (1 + g * (1 - s)),   du = dh * g * s
+ *   dh      bf16 [tokens, inner]
+ *   cq, cs  the checkpoint taco_swiglu_quantize wrote
+ *   dgu     out: bf16 [tokens, 2 * inner], dg then du
+ *   dq, ds  out: [tokens, 2 * inner] in the block format, from dg and du before
+ *           their rounding to bf16.  Both NULL: not written.
+ */
+taco_status_t taco_swiglu_backward(const void* dh_bf16, const uint8_t* cq, const uint8_t* cs,
+                                   int64_t tokens, int64_t inner, void* dgu_bf16, uint8_t* dq,
+                                   uint8_t* ds, taco_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* TACO_LINEAR_H */
