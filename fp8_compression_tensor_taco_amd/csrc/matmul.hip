@@ -2,6 +2,7 @@
 // the FP8 product of quantised rows with a quantised weight, and the weight
 // gradient from the quantised rows.
 #include <algorithm>
+#include <type_traits>
 
 #include "blockfmt.h"
 
@@ -13,54 +14,497 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 256;
 
+// ------------------------------------------------------------------ FP8 product
+//
 // y[m, n] = a[m, :] . b[n, :].  v_mfma_scale_f32_16x16x128_f8f6f4 takes 128
 // columns of 16 rows of both operands, one block each, and multiplies the two
-// blocks' scales in.  b is the first operand, so a lane ends with four
-// consecutive n of one row of y.  Lane l holds row l % 16 of an operand and
-// columns 32 (l / 16) + 0..31.
-__global__ __launch_bounds__(kThreads) void matmul_fp8_kernel(const uint8_t* __restrict__ qa, const uint8_t* __restrict__ sa,
-                                                              const uint8_t* __restrict__ qb, const uint8_t* __restrict__ sb,
-                                                              int m, int n, int kcols, int kscales,
-                                                              uint16_t* __restrict__ y) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r = lane & 15, g = lane >> 4;
-  const int64_t tiles_n = (n + 31) / 32;
-  const int64_t tile = static_cast<int64_t>(blockIdx.x) * 4 + wave;
-  const int64_t tm = tile / tiles_n;
-  const int m0 = static_cast<int>(tm) * 32, n0 = static_cast<int>(tile - tm * tiles_n) * 32;
-  if (m0 >= m) return;
-  f32x4_t acc[2][2] = {};
-  const uint8_t* ap[2], *bp[2], *as[2], *bs[2];
+// blocks' scales in, so the whole sum over k stays in one fp32 accumulator and
+// the scales cost no vector instruction.  (The instruction aligns the products
+// of eight consecutive columns to the largest of them and keeps 13 bits below
+// it: a relative error near 3e-5 on normal data, under the 2^-9 of the output's
+// rounding.)  b is the first operand, so a lane ends with four consecutive n of
+// one row of y.
+
+__device__ __forceinline__ unsigned lds_address(const void* p) {
+  return static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
+}
+
+// A wave-uniform pointer, kept in scalar registers.
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint64_t lo = static_cast<unsigned>(__builtin_amdgcn_readfirstlane(static_cast<int>(v)));
+  const uint64_t hi = static_cast<unsigned>(__builtin_amdgcn_readfirstlane(static_cast<int>(v >> 32)));
+  return reinterpret_cast<const uint8_t*>(hi << 32 | lo);
+}
+
+// Lane i copies the 16 bytes at base + off to LDS address lds + 16 i.  Inline
+// assembly, because with the builtin the compiler waits for every copy in
+// flight before the next LDS read; the reads are ordered by wait_copies and
+// barriers instead.  No register is written, so nothing can be reused early.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void copy16_to_lds(const uint8_t* base, unsigned off, unsigned lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(off), "s"(base), "s"(lds) : "memory", "m0");
+#endif
+}
+// The same with 4 bytes per lane, to lds + 4 i.
+__device__ __forceinline__ void copy4_to_lds(const uint8_t* base, unsigned off, unsigned lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :: "v"(off), "s"(base), "s"(lds) : "memory", "m0");
+#endif
+}
+#pragma clang diagnostic pop
+
+// The tile of a workgroup.  Workgroups go to the eight XCDs in turn, so every
+// eighth one shares an L2: each XCD takes one contiguous run of the tiles, in
+// bands of kBand tiles of a by all of b's, where neighbours share operands.
+constexpr int kBand = 4;
+__device__ __forceinline__ void tile_of_block(int tiles_m, int tiles_n, int& tile_m, int& tile_n) {
+  const int total = static_cast<int>(gridDim.x), block = static_cast<int>(blockIdx.x);
+  const int per = total / 8, more = total % 8, xcd = block % 8;
+  const int t = xcd * per + min(xcd, more) + block / 8;
+  const int band = t / (kBand * tiles_n), in = t - band * kBand * tiles_n;
+  const int rows = min(kBand, tiles_m - kBand * band);
+  tile_n = __builtin_amdgcn_readfirstlane(in / rows);
+  tile_m = __builtin_amdgcn_readfirstlane(kBand * band + in - tile_n * rows);
+}
+
+// 128 columns of the rows of an operand in LDS: 128 bytes per row, the 16-byte
+// chunk c of row r at position c ^ (r % 8), so the 16 rows of a fragment read
+// spread over all banks.  Lane l of a copy fills position l % 8 of row l / 8 of
+// its eight rows, so it fetches chunk (l % 8) ^ (l / 8).
+//
+// A fragment: lane l holds row l % 16, chunks g = l / 16 and g + 4 of it.  The
+// instruction's own order of the 128 columns does not matter, since both
+// operands share it and the scale is the same for all of them.
+__device__ __forceinline__ i32x8_t load_fragment(const uint8_t* tile, int lane_off) {
+  const int4 lo = *reinterpret_cast<const int4*>(tile + lane_off);
+  const int4 hi = *reinterpret_cast<const int4*>(tile + (lane_off ^ 64));
+  return i32x8_t{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+}
+
+template <int N>
+__device__ __forceinline__ void copies_left() {   // at most N of the wavefront's copies are in flight
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
+__device__ __forceinline__ void meet() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
+__device__ __forceinline__ void reads_done_and_meet() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
+template <int NT, int MT>
+__device__ __forceinline__ void multiply(const i32x8_t (&b)[NT], const i32x8_t (&a)[MT], int sb, const int (&sa)[MT],
+                                         f32x4_t* acc) {
+  __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t am = min(m0 + 16 * i + r, m - 1), bn = min(n0 + 16 * i + r, n - 1);
-    ap[i] = qa + am * kcols + 32 * g;
-    bp[i] = qb + bn * kcols + 32 * g;
-    as[i] = sa + am * kscales;
-    bs[i] = sb + bn / kBlock * kscales;
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+      acc[i * MT + j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[i], a[j], acc[i * MT + j], 0, 0, 0, sb, 0, sa[j]);
+  __builtin_amdgcn_s_setprio(0);
+}
+
+// Four consecutive columns of a row of y, from `col` on.  Rows of odd length
+// start at any element: the store is 8 bytes at 2-byte alignment.
+__device__ __forceinline__ void store_columns(uint16_t* out, int col, int n, const f32x4_t v) {
+  const uint2 u = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  if (col + 4 <= n) {
+    __builtin_memcpy(out + col, &u, 8);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 3; ++c)
+      if (col + c < n) out[col + c] = static_cast<uint16_t>((c < 2 ? u.x : u.y) >> (16 * (c & 1)));
   }
-  for (int kb = 0; kb < kcols / kBlock; ++kb) {
-    i32x8_t a[2], b[2];
+}
+
+// The middle sizes: tiles of BN = 16 NT WN rows of b and BM = 16 MT WM rows of
+// a.  KG groups of WN x WM wavefronts share a tile and take the steps in turn,
+// which keeps a CU's memory pipeline busy where there are few tiles; their sums
+// are added in LDS at the end, in the groups' order.  Each group has a ring of
+// S steps in LDS, S - 1 of them on their way; one barrier per round of steps.
+template <int NT, int MT, int WN, int WM, int KG, int S>
+struct MatmulTile {
+  static constexpr int kGroup = WN * WM, kThreads = 64 * kGroup * KG;
+  static constexpr int BN = 16 * NT * WN, BM = 16 * MT * WM;
+  static constexpr int kOperands = (BN + BM) * kBlock;          // bytes of one step
+  static constexpr int kScales = 512;                           // per wavefront: its rows' dwords, its block's
+  static constexpr int kPeriod = 4 / KG;                        // rounds that a dword of scale bytes serves
+  static constexpr int kCopiesB = BN / 8 / kGroup, kCopiesA = BM / 8 / kGroup;
+  static constexpr int kCopies = kCopiesB + kCopiesA;           // per wavefront and step
+  static constexpr int kLds = KG * S * kOperands + 2 * KG * kGroup * kScales;
+  static_assert(BN % (8 * kGroup) == 0 && BM % (8 * kGroup) == 0, "whole copies of one operand");
+  static_assert(16 * NT <= kBlock && kBlock % (16 * NT) == 0, "a wavefront's rows of b share their scale");
+  static_assert(16 * MT <= 64, "a lane per row of a in a copy of scales");
+  static_assert(S >= 2 && S - 2 <= kPeriod, "the next scales are older than the S - 2 newest steps when they are due");
+  static_assert((KG - 1) * kGroup * NT * MT * 1024 <= kLds, "the groups' sums fit where the operands were");
+};
+
+template <int NT, int MT, int WN, int WM, int KG, int S>
+__global__ __launch_bounds__(64 * WN * WM * KG) void matmul_tiles_kernel(
+    const uint8_t* __restrict__ qa, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ qb,
+    const uint8_t* __restrict__ sb, int m, int n, int kcols, int kscales, uint16_t* __restrict__ y) {
+  using T = MatmulTile<NT, MT, WN, WM, KG, S>;
+  __shared__ __align__(128) uint8_t lds[T::kLds];
+  const int lane = threadIdx.x & 63;
+  const int any_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = any_wave / T::kGroup, wave = any_wave % T::kGroup;
+  int tile_m, tile_n;
+  tile_of_block((m + T::BM - 1) / T::BM, (n + T::BN - 1) / T::BN, tile_m, tile_n);
+  const int m0 = tile_m * T::BM, n0 = tile_n * T::BN;
+  const int r = lane & 15, g = lane >> 4;
+  const int wn = wave % WN, wm = wave / WN;
+
+  // Copies: the step's rows (b's, then a's) in groups of eight, consecutive
+  // ones per wavefront for each operand.  Rows past the end are read from the
+  // last row; what they give is never stored.  Every kPeriod rounds a wavefront
+  // also copies the next dword of scale bytes of each of its rows of a (a lane
+  // each) and of its block of b (all lanes alike), into the other of its two
+  // buffers.
+  const uint8_t* gb = uniform(qb + static_cast<int64_t>(n0) * kcols);
+  const uint8_t* ga = uniform(qa + static_cast<int64_t>(m0) * kcols);
+  const uint8_t* gsa = uniform(sa + static_cast<int64_t>(m0) * kscales);
+  const uint8_t* gsb = uniform(sb + static_cast<int64_t>(min(n0 + 16 * NT * wn, n - 1) / kBlock) * kscales);
+  const int left_n = n - 1 - n0, left_m = m - 1 - m0;
+  unsigned off_b[T::kCopiesB], off_a[T::kCopiesA];
+  const unsigned chunk = 16 * ((lane & 7) ^ (lane >> 3));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      a[i] = *reinterpret_cast<const i32x8_t*>(ap[i] + kb * kBlock);
-      b[i] = *reinterpret_cast<const i32x8_t*>(bp[i] + kb * kBlock);
+  for (int i = 0; i < T::kCopiesB; ++i)
+    off_b[i] = static_cast<unsigned>(min(8 * (wave * T::kCopiesB + i) + (lane >> 3), left_n)) * kcols + chunk;
+#pragma unroll
+  for (int i = 0; i < T::kCopiesA; ++i)
+    off_a[i] = static_cast<unsigned>(min(8 * (wave * T::kCopiesA + i) + (lane >> 3), left_m)) * kcols + chunk;
+  const unsigned off_s = static_cast<unsigned>(min(16 * MT * wm + (lane & (16 * MT - 1)), left_m)) * kscales;
+  const unsigned lds0 = lds_address(lds) + group * S * T::kOperands;
+  auto copy_step = [&](int k, int slot) {
+    const unsigned at = lds0 + slot * T::kOperands;
+#pragma unroll
+    for (int i = 0; i < T::kCopiesB; ++i) copy16_to_lds(gb + k * kBlock, off_b[i], at + 1024 * (wave * T::kCopiesB + i));
+#pragma unroll
+    for (int i = 0; i < T::kCopiesA; ++i)
+      copy16_to_lds(ga + k * kBlock, off_a[i], at + T::BN * kBlock + 1024 * (wave * T::kCopiesA + i));
+  };
+  const int scales0 = KG * S * T::kOperands + 2 * any_wave * T::kScales;
+  auto copy_scales = [&](int k) {
+    const unsigned at = lds_address(lds) + scales0 + (k >> 2 & 1) * T::kScales;
+    copy4_to_lds(gsa + (k & ~3), off_s, at);
+    copy4_to_lds(gsb + (k & ~3), 0, at + 256);
+  };
+
+  const int lane_off = r * kBlock + 16 * (g ^ (r & 7));
+  f32x4_t acc[NT][MT] = {};
+  const int steps = kcols / kBlock;
+  if (group < steps) copy_scales(group);
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i)
+    if (group + i * KG < steps) copy_step(group + i * KG, i);
+  int slot = 0, round = 0;
+  for (int k = group; k < steps + group; k += KG, ++round) {
+    // step k has landed for all; what the step before it read has been multiplied
+    if (k + (S - 2) * KG < steps)
+      copies_left<(S - 2) * T::kCopies>();
+    else
+      copies_left<0>();
+    meet();
+    if (round % T::kPeriod == 0 && k + T::kPeriod * KG < steps) copy_scales(k + T::kPeriod * KG);
+    if (k + (S - 1) * KG < steps) copy_step(k + (S - 1) * KG, slot == 0 ? S - 1 : slot - 1);
+    if (k < steps) {
+      const uint8_t* stage = lds + (group * S + slot) * T::kOperands;
+      const uint8_t* tb = stage + 16 * NT * wn * kBlock;
+      const uint8_t* ta = stage + (T::BN + 16 * MT * wm) * kBlock;
+      const uint8_t* scales = lds + scales0 + (k >> 2 & 1) * T::kScales + (k & 3);
+      i32x8_t a[MT], b[NT];
+      int scale_a[MT];
+#pragma unroll
+      for (int j = 0; j < MT; ++j) scale_a[j] = scales[4 * (16 * j + r)];
+      const int scale_b = scales[256];
+#pragma unroll
+      for (int j = 0; j < MT; ++j) a[j] = load_fragment(ta + 16 * kBlock * j, lane_off);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) b[i] = load_fragment(tb + 16 * kBlock * i, lane_off);
+      multiply(b, a, scale_b, scale_a, &acc[0][0]);
+    }
+    slot = slot + 1 == S ? 0 : slot + 1;
+  }
+  if constexpr (KG > 1) {
+    f32x4_t* sums = reinterpret_cast<f32x4_t*>(lds);      // [group - 1][wavefront][tile][lane]
+    __syncthreads();
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < NT * MT; ++i) sums[(((group - 1) * T::kGroup + wave) * NT * MT + i) * 64 + lane] = (&acc[0][0])[i];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int q = 0; q < KG - 1; ++q)
+#pragma unroll
+      for (int i = 0; i < NT * MT; ++i) (&acc[0][0])[i] += sums[((q * T::kGroup + wave) * NT * MT + i) * 64 + lane];
+  }
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int row = m0 + 16 * (MT * wm + j) + r;
+    if (row >= m) continue;
+    uint16_t* out = y + static_cast<int64_t>(row) * n;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) store_columns(out, n0 + 16 * (NT * wn + i) + 4 * g, n, acc[i][j]);
+  }
+}
+
+// Few rows of a (at most 16 MT): every byte of b is used once, so the weight's
+// stream from HBM is the time.  A workgroup takes 16 rows of b and its
+// wavefronts split k, each reading its fragments straight into registers,
+// kAhead steps at a time; the partial sums are added in LDS in the wavefronts'
+// order.  No barrier but that one, no copy through LDS.  4 x 4096 x 4096: 5.4 us
+// over weights that are in the last-level cache (3.1 TB/s; launch and latency are
+// about half of it), 1 x 14336 x 3584: 12.0 us (4.3 TB/s).
+constexpr int kFewWaves = 8;
+template <int MT>
+__global__ __launch_bounds__(64 * kFewWaves) void matmul_few_kernel(
+    const uint8_t* __restrict__ qa, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ qb,
+    const uint8_t* __restrict__ sb, int m, int n, int kcols, int kscales, uint16_t* __restrict__ y) {
+  constexpr int kAhead = 4;
+  __shared__ __align__(16) f32x4_t part[kFewWaves][MT][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * 16, steps = kcols / kBlock;
+  const uint8_t* bp = qb + static_cast<int64_t>(min(n0 + r, n - 1)) * kcols + 16 * g;
+  const uint8_t* bs = sb + static_cast<int64_t>(n0 / kBlock) * kscales;
+  const uint8_t *ap[MT], *as[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int64_t row = min(16 * j + r, m - 1);
+    ap[j] = qa + row * kcols + 16 * g;
+    as[j] = sa + row * kscales;
+  }
+  auto fragment = [](const uint8_t* p) {              // chunks g and g + 4 of a row's 128 columns
+    const int4 lo = *reinterpret_cast<const int4*>(p), hi = *reinterpret_cast<const int4*>(p + 64);
+    return i32x8_t{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  };
+  f32x4_t acc[MT] = {};
+  for (int k0 = wave; k0 < steps; k0 += kFewWaves * kAhead) {
+    i32x8_t b[kAhead], a[kAhead][MT];
+    int scale_b[kAhead], scale_a[kAhead][MT];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = min(k0 + u * kFewWaves, steps - 1);
+      b[u] = fragment(bp + static_cast<int64_t>(k) * kBlock);
+      scale_b[u] = bs[k];
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        a[u][j] = fragment(ap[j] + static_cast<int64_t>(k) * kBlock);
+        scale_a[u][j] = as[j][k];
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int u = 0; u < kAhead; ++u)
+      if (k0 + u * kFewWaves < steps) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a[i], acc[i][j], 0, 0, 0, bs[j][kb], 0, as[i][kb]);
+        for (int j = 0; j < MT; ++j)
+          acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[u], a[u][j], acc[j], 0, 0, 0, scale_b[u], 0, scale_a[u][j]);
+      }
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int j = 0; j < MT; ++j) part[wave][j][lane] = acc[j];
+  __syncthreads();
+  for (int j = wave; j < MT; j += kFewWaves) {
+    f32x4_t v = part[0][j][lane];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int w = 1; w < kFewWaves; ++w) v += part[w][j][lane];
+    const int row = 16 * j + r;
+    if (row < m) store_columns(y + static_cast<int64_t>(row) * n, n0 + 4 * g, n, v);
+  }
+}
+
+// The large product: 256 x 256 tiles, 8 wavefronts of 128 rows of b by 64 of a.
+//
+// Two groups of wavefronts take turns.  A SIMD holds one wavefront of each
+// group; while one group's matrix instructions run, the other reads its next
+// fragments, so neither the LDS latency nor the reads' bandwidth shows.  A step
+// (128 columns) has four phases with a barrier of the whole workgroup after
+// each: M1, read a's fragments and the first half of b's; C1, multiply; M2,
+// read b's second half; C2, multiply.  The second group runs one phase behind.
+//
+// The operands stream through a ring of nine 16 KiB units in LDS, four per
+// step in the order b's first halves, a's rows 0..127, a's rows 128..255, b's
+// second halves.  Unit u goes to slot u % 9 once unit u - 9 has been read by
+// both groups.  Each phase issues one unit, two copies per wavefront, so the
+// copies reach the memory pipeline evenly: with P1..P4 the first group's M1(k),
+// C1(k), M2(k), C2(k) and the second's C2(k - 1), M1(k), C1(k), M2(k), they are
+// units 4 k + 7..4 k + 10.  Before the barrier that frees a unit for reading,
+// every wavefront waits until only newer units are in flight: at the end of P2
+// unit 4 k + 3 is due and five are newer, at the end of P4 unit 4 k + 6 with
+// four newer.  Copies retire in issue order, so operations issued later only
+// make a wait stricter.
+//
+// 8192 x 8192 x 8192: 400 us, 2.75 PFLOP/s; 8192 x 14336 x 3584: 350 us, 2.4.
+// Without the loop's copies 8192^3 takes 324 us, without the LDS reads 321, the
+// copies alone 206: the two compete for LDS and the barriers cost the rest.
+// With one step in flight (two whole buffers) it took 435 us, with a step's
+// copies issued at once 425.
+constexpr int kBig = 256;                       // rows of either operand in a tile
+constexpr int kUnit = 128 * kBlock;             // bytes: 128 rows of 128 columns
+constexpr int kRing = 9;
+constexpr int kScaleBuffer = 2048;              // a dword of scale bytes (four steps) for each row, twice over
+
+__global__ __launch_bounds__(512) void matmul_turns_kernel(
+    const uint8_t* __restrict__ qa, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ qb,
+    const uint8_t* __restrict__ sb, int m, int n, int kcols, int kscales, uint16_t* __restrict__ y) {
+  constexpr int NT = 8, MT = 4;
+  __shared__ __align__(128) uint8_t lds[kRing * kUnit + 2 * kScaleBuffer];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles_m = (m + kBig - 1) / kBig, tiles_n = (n + kBig - 1) / kBig;
+  int tile_m, tile_n;
+  tile_of_block(tiles_m, tiles_n, tile_m, tile_n);
+  const int m0 = tile_m * kBig, n0 = tile_n * kBig;
+  const int r = lane & 15, g = lane >> 4;
+  const int wn = wave & 1, wm = wave >> 1;
+
+  // Copies: a wavefront fills rows 16 wave + 0..15 of every unit.  Rows past
+  // the end are read from the last row; what they give is never stored.
+  const uint8_t* gb = uniform(qb + static_cast<int64_t>(n0) * kcols);
+  const uint8_t* ga = uniform(qa + static_cast<int64_t>(m0) * kcols);
+  const int left_n = n - 1 - n0, left_m = m - 1 - m0;
+  unsigned off_b1[2], off_b2[2], off_a1[2], off_a2[2];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int row = m0 + 16 * i + r, col = n0 + 16 * j + 4 * g + c;
-        if (row < m && col < n) y[static_cast<int64_t>(row) * n + col] = static_cast<uint16_t>(pack_bf16x2(acc[i][j][c], 0.0f));
+  for (int i = 0; i < 2; ++i) {
+    const int row = 16 * wave + 8 * i + (lane >> 3), row_b = (row & 64) + row;     // b: 64 rows of each half tile
+    const unsigned chunk = 16 * ((lane & 7) ^ (lane >> 3));
+    off_b1[i] = static_cast<unsigned>(min(row_b, left_n)) * kcols + chunk;
+    off_b2[i] = static_cast<unsigned>(min(row_b + 64, left_n)) * kcols + chunk;
+    off_a1[i] = static_cast<unsigned>(min(row, left_m)) * kcols + chunk;
+    off_a2[i] = static_cast<unsigned>(min(row + 128, left_m)) * kcols + chunk;
+  }
+  // Scale bytes: wavefronts 0..3 take a dword of 64 rows of a each, the others
+  // (all alike) the dwords of b's two blocks.
+  const uint8_t* gs = uniform(wave < 4 ? sa + static_cast<int64_t>(m0) * kscales
+                                       : sb + static_cast<int64_t>(n0 / kBlock) * kscales);
+  const unsigned off_s = (wave < 4 ? static_cast<unsigned>(min(64 * wave + lane, left_m))
+                                   : static_cast<unsigned>(min(lane & 1, left_n / kBlock))) * kscales;
+  const unsigned lds0 = lds_address(lds) + 2048 * wave;
+  const unsigned lds_s = lds_address(lds) + kRing * kUnit + 256 * wave;
+  auto copy_unit = [&](const uint8_t* base, const unsigned (&off)[2], int k, int slot) {
+    copy16_to_lds(base + k * kBlock, off[0], lds0 + slot * kUnit);
+    copy16_to_lds(base + k * kBlock, off[1], lds0 + slot * kUnit + 1024);
+  };
+  auto copy_scales = [&](int k) { copy4_to_lds(gs + k, off_s, lds_s + (k >> 2 & 1) * kScaleBuffer); };
+  auto slot_after = [](int slot, int d) { return slot + d >= kRing ? slot + d - kRing : slot + d; };
+
+  const int lane_off = r * kBlock + 16 * (g ^ (r & 7));
+  f32x4_t acc[NT][MT] = {};
+  const int steps = kcols / kBlock;
+  copy_scales(0);
+  copy_unit(gb, off_b1, 0, 0);
+  copy_unit(ga, off_a1, 0, 1);
+  copy_unit(ga, off_a2, 0, 2);
+  copy_unit(gb, off_b2, 0, 3);
+  if (steps > 1) {
+    copy_unit(gb, off_b1, 1, 4);
+    copy_unit(ga, off_a1, 1, 5);
+    copy_unit(ga, off_a2, 1, 6);
+    copies_left<8>();
+  } else {
+    copies_left<2>();
+  }
+  meet();
+
+  auto run = [&](auto group) {
+    constexpr bool kSecond = group.value;
+    int slot = 0;                                  // of the step's first unit
+    if constexpr (kSecond) {
+      if (steps > 1) copy_unit(gb, off_b2, 1, 7);
+      meet();
+    }
+    // TAIL 0: steps that have two more after them, 1: the last but one, 2: the last.
+    auto step = [&](int k, auto tail) {
+      constexpr int TAIL = tail.value;
+      const uint8_t* scales = lds + kRing * kUnit + (k >> 2 & 1) * kScaleBuffer + (k & 3);
+      const uint8_t* tb = lds + slot * kUnit + 64 * kBlock * wn;
+      const uint8_t* ta = lds + slot_after(slot, wm < 2 ? 1 : 2) * kUnit + 64 * kBlock * (wm & 1);
+      const uint8_t* tb2 = lds + slot_after(slot, 3) * kUnit + 64 * kBlock * wn;
+      auto p1_copy = [&](int at, int s) { copy_unit(gb, off_b2, at + 1, slot_after(s, 7)); };
+      auto p2_copy = [&] {
+        if constexpr (TAIL == 0) {
+          if ((k & 3) == 0 && k + 4 < steps) copy_scales(k + 4);
+          copy_unit(gb, off_b1, k + 2, slot_after(slot, 8));
+        }
+      };
+      auto p3_copy = [&] { if constexpr (TAIL == 0) copy_unit(ga, off_a1, k + 2, slot); };
+      auto p4_copy = [&] { if constexpr (TAIL == 0) copy_unit(ga, off_a2, k + 2, slot_after(slot, 1)); };
+      auto p2_wait = [&] { copies_left<TAIL == 0 ? 10 : TAIL == 1 ? 8 : 0>(); };   // this step's last unit
+      auto p4_wait = [&] { copies_left<TAIL == 0 ? 8 : TAIL == 1 ? 2 : 0>(); };    // the next step's first three
+      i32x8_t a[MT], b[NT / 2];
+      int scale_a[MT];
+#pragma unroll
+      for (int i = 0; i < NT / 2; ++i) b[i] = load_fragment(tb + 16 * kBlock * i, lane_off);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) a[j] = load_fragment(ta + 16 * kBlock * j, lane_off);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) scale_a[j] = scales[4 * (64 * wm + 16 * j + r)];
+      const int scale_b = scales[1024 + 4 * wn];
+      if constexpr (kSecond) {
+        p2_copy();
+        p2_wait();
+      } else if constexpr (TAIL < 2) {
+        p1_copy(k, slot);
       }
+      reads_done_and_meet();
+      if constexpr (kSecond) p3_copy(); else p2_copy();
+      multiply(b, a, scale_b, scale_a, &acc[0][0]);
+      if constexpr (!kSecond) p2_wait();
+      meet();
+#pragma unroll
+      for (int i = 0; i < NT / 2; ++i) b[i] = load_fragment(tb2 + 16 * kBlock * i, lane_off);
+      if constexpr (kSecond) {
+        p4_copy();
+        p4_wait();
+      } else {
+        p3_copy();
+      }
+      reads_done_and_meet();
+      if constexpr (!kSecond) p4_copy(); else if constexpr (TAIL == 0) p1_copy(k + 1, slot_after(slot, 4));
+      multiply(b, a, scale_b, scale_a, &acc[NT / 2][0]);
+      if constexpr (!kSecond) p4_wait();
+      meet();
+      slot = slot_after(slot, 4);
+    };
+    int k = 0;
+    for (; k + 2 < steps; ++k) step(k, std::integral_constant<int, 0>{});
+    if (steps > 1) step(steps - 2, std::integral_constant<int, 1>{});
+    step(steps - 1, std::integral_constant<int, 2>{});
+    if constexpr (!kSecond) meet();
+  };
+  if (wave >= 4)
+    run(std::true_type{});
+  else
+    run(std::false_type{});
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int row = m0 + 16 * (MT * wm + j) + r;
+    if (row >= m) continue;
+    uint16_t* out = y + static_cast<int64_t>(row) * n;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) store_columns(out, n0 + 16 * (NT * wn + i) + 4 * g, n, acc[i][j]);
+  }
 }
 
 // dw[n, k] = sum over t of dy[t, n] * x[t, k], a 64 x 64 tile per workgroup, 32
@@ -105,6 +549,66 @@ __global__ __launch_bounds__(kThreads) void wgrad_fp8_kernel(const uint16_t* __r
     }
 }
 
+struct MatmulArgs {
+  const uint8_t *qa, *sa, *qb, *sb;
+  int m, n, kcols, kscales;
+  uint16_t* y;
+};
+
+int64_t tiles_of(int64_t m, int64_t n, int64_t bm, int64_t bn) { return (m + bm - 1) / bm * ((n + bn - 1) / bn); }
+
+template <int MT>
+void launch_few(const MatmulArgs& p, hipStream_t stream) {
+  hipLaunchKernelGGL(matmul_few_kernel<MT>, dim3((p.n + 15) / 16), dim3(64 * kFewWaves), 0, stream, p.qa, p.sa, p.qb,
+                     p.sb, p.m, p.n, p.kcols, p.kscales, p.y);
+}
+
+template <int NT, int MT, int WN, int WM, int KG, int S>
+void launch_tiles(const MatmulArgs& p, hipStream_t stream) {
+  using T = MatmulTile<NT, MT, WN, WM, KG, S>;
+  hipLaunchKernelGGL((matmul_tiles_kernel<NT, MT, WN, WM, KG, S>),
+                     dim3(static_cast<unsigned>(tiles_of(p.m, p.n, T::BM, T::BN))), dim3(T::kThreads), 0, stream, p.qa,
+                     p.sa, p.qb, p.sb, p.m, p.n, p.kcols, p.kscales, p.y);
+}
+
+void launch_big(const MatmulArgs& p, hipStream_t stream) {
+  hipLaunchKernelGGL(matmul_turns_kernel, dim3(static_cast<unsigned>(tiles_of(p.m, p.n, kBig, kBig))), dim3(512), 0,
+                     stream, p.qa, p.sa, p.qb, p.sb, p.m, p.n, p.kcols, p.kscales, p.y);
+}
+
+// Which kernel: by the number of tiles against the 256 CUs.  Measured (us):
+//   m     n     k      64x64 KG 2  64x64 KG 1  128x128 KG 2  128x128 KG 1  256x256
+//   256   4096  4096   10.8        13.1        20.8          25.3          45.8
+//   777   1601  1600   12.2        9.3         13.2          14.6          32.0
+//   512   4096  4096   20.3        16.6        20.9          25.6          46.2
+//   1024  4096  4096   38.8        30.5        22.0          26.1          46.7
+//   2048  4096  4096   76.0        55.6        42.2          35.0          47.9
+//   4096  4096  4096   154         112         107           78.0          59.7
+//   8192  3584  1000   105         58.6        56.1          44.5          42.5
+// so 64 x 64 tiles until a CU would have more than three, two groups of
+// wavefronts for a tile where a CU has one.  A round of 256 large tiles takes
+// 1.65 times as long as a round of 512 of 128 x 128, whose leftovers cost less.
+// Up to 32 rows the direct loads win (16 rows: 6.7 against 9.7, 32: 9.5 against
+// 10.0), and at 64 rows the tiles do (15.2 against 10.6).
+void launch_matmul(const MatmulArgs& p, hipStream_t stream) {
+  const int64_t t64 = tiles_of(p.m, p.n, 64, 64), t128 = tiles_of(p.m, p.n, 128, 128);
+  const int64_t rounds_big = (tiles_of(p.m, p.n, kBig, kBig) + 255) / 256;
+  if (p.m <= 16)
+    launch_few<1>(p, stream);
+  else if (p.m <= 32)
+    launch_few<2>(p, stream);
+  else if (t64 <= 256)
+    launch_tiles<2, 2, 2, 2, 2, 4>(p, stream);
+  else if (t64 <= 768)
+    launch_tiles<2, 2, 2, 2, 1, 3>(p, stream);
+  else if (t128 <= 256)
+    launch_tiles<4, 4, 2, 2, 2, 2>(p, stream);
+  else if (845 * rounds_big > t128)
+    launch_tiles<4, 4, 2, 2, 1, 2>(p, stream);
+  else
+    launch_big(p, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -125,10 +629,8 @@ taco_status_t taco_matmul_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_
               {{qa, static_cast<size_t>(m * kcols)}, {sa, static_cast<size_t>(m * kscales)},
                {qb, static_cast<size_t>(n * kcols)}, {sb, static_cast<size_t>((n + kBlock - 1) / kBlock * kscales)}}))
     return TACO_ERR_ALIAS;
-  const int64_t tiles = (m + 31) / 32 * ((n + 31) / 32);
-  hipLaunchKernelGGL(matmul_fp8_kernel, dim3(static_cast<unsigned>((tiles + 3) / 4)), dim3(kThreads), 0, stream, qa, sa,
-                     qb, sb, static_cast<int>(m), static_cast<int>(n), static_cast<int>(kcols),
-                     static_cast<int>(kscales), static_cast<uint16_t*>(y_bf16));
+  launch_matmul({qa, sa, qb, sb, static_cast<int>(m), static_cast<int>(n), static_cast<int>(kcols),
+                 static_cast<int>(kscales), static_cast<uint16_t*>(y_bf16)}, stream);
   return launched();
 }
 

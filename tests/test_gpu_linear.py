@@ -227,6 +227,24 @@ def test_matmul_exact_sums(m, n, k):
     assert (f64(y) == oracle.bf16_bits_to_f64(oracle.f64_to_bf16_bits(v))).all()
 
 
+# enough tiles for the larger kernels (64 x 64 and 128 x 128 tiles of one or two groups of wavefronts, 256 x 256), and
+# every start and end of their pipelines: 1, 2, 3, 4, 5, 9 and 13 blocks of k
+@pytest.mark.parametrize("k", [100, 256, 300, 512, 600, 1100, 1600])
+@pytest.mark.parametrize("m,n", [(40, 130), (450, 3000), (1900, 1980), (2100, 2203), (3700, 3901)])
+def test_matmul_exact_sums_of_many_tiles(m, n, k):
+    rng = np.random.default_rng(m + k)
+    wide, sc = ol.padded(k), ol.scale_cols(k)
+    values = np.array([0x00, 0x38, 0x3C, 0x40, 0xB8, 0xBC, 0xC0], np.uint8)          # 0, +-1, +-1.5, +-2
+    qa, qb = (values[rng.integers(0, 7, (r, wide))] for r in (m, n))
+    sa, sb = rng.integers(127, 129, (m, sc)).astype(np.uint8), rng.integers(127, 129, (-(-n // 128), sc)).astype(np.uint8)
+    whole, out = guarded((m, n), torch.bfloat16)
+    y = taco.matmul_fp8(*(torch.from_numpy(t).cuda() for t in (qa, sa, qb, sb)), out=out)
+    a = torch.from_numpy(ol.row_values(qa, sa)).float()
+    b = torch.from_numpy(ol.weight_values(qb, sb)).float()
+    want = (a @ b.t()).to(torch.bfloat16)            # exact in fp32: multiples of 1/4 below 2^18
+    assert torch.equal(y.cpu(), want) and survived(whole)
+
+
 @pytest.mark.parametrize("m,n,k", [(2, 200, 300), (150, 200, 640), (300, 520, 256)])
 def test_matmul_any_codes_and_scales(m, n, k):
     """Every code but NaN, scale bytes over a wide range, differing from block to block."""
