@@ -12,8 +12,6 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
-constexpr int kThreads = 256;
-
 // ------------------------------------------------------------------ FP8 product
 //
 // y[m, n] = a[m, :] . b[n, :].  v_mfma_scale_f32_16x16x128_f8f6f4 takes 128
@@ -35,6 +33,18 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
   const uint64_t lo = static_cast<unsigned>(__builtin_amdgcn_readfirstlane(static_cast<int>(v)));
   const uint64_t hi = static_cast<unsigned>(__builtin_amdgcn_readfirstlane(static_cast<int>(v >> 32)));
   return reinterpret_cast<const uint8_t*>(hi << 32 | lo);
+}
+
+// A load at a wave-uniform base and a 32-bit offset, any alignment of 2 bytes.
+typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
+typedef u32x4_t u32x4_loose_t __attribute__((aligned(2)));
+#define TACO_GLOBAL __attribute__((address_space(1)))
+__device__ __forceinline__ uint4 load16_at(const uint8_t* base, unsigned off) {
+  const auto* p = reinterpret_cast<const TACO_GLOBAL uint8_t*>(reinterpret_cast<uint64_t>(base));
+  return __builtin_bit_cast(uint4, u32x4_t(*reinterpret_cast<const TACO_GLOBAL u32x4_loose_t*>(p + off)));
+}
+__device__ __forceinline__ unsigned load1_at(const uint8_t* base, unsigned off) {
+  return reinterpret_cast<const TACO_GLOBAL uint8_t*>(reinterpret_cast<uint64_t>(base))[off];
 }
 
 // Lane i copies the 16 bytes at base + off to LDS address lds + 16 i.  Inline
@@ -70,6 +80,16 @@ __device__ __forceinline__ void tile_of_block(int tiles_m, int tiles_n, int& til
   const int rows = min(kBand, tiles_m - kBand * band);
   tile_n = __builtin_amdgcn_readfirstlane(in / rows);
   tile_m = __builtin_amdgcn_readfirstlane(kBand * band + in - tile_n * rows);
+}
+
+__device__ __forceinline__ void opaque(int& v) { asm volatile("" : "+v"(v)); }
+
+// The compiler moves no memory access or matrix instruction across.
+__device__ __forceinline__ void fence() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+#endif
 }
 
 // 128 columns of the rows of an operand in LDS: 128 bytes per row, the 16-byte
@@ -507,46 +527,348 @@ __global__ __launch_bounds__(512) void matmul_turns_kernel(
   }
 }
 
-// dw[n, k] = sum over t of dy[t, n] * x[t, k], a 64 x 64 tile per workgroup, 32
-// tokens per step, both operands turned in LDS.
-__global__ __launch_bounds__(kThreads) void wgrad_fp8_kernel(const uint16_t* __restrict__ dy, const uint8_t* __restrict__ q,
-                                                             const uint8_t* __restrict__ scale, int tokens, int n, int k,
-                                                             int kcols, int kscales, float* __restrict__ dw, int accumulate) {
-  __shared__ __align__(16) uint16_t td[64][40], tx[64][40];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r = lane & 15, g = lane >> 4;
-  const int tiles_k = (k + 63) / 64;
-  const int n0 = static_cast<int>(blockIdx.x / tiles_k) * 64, k0 = static_cast<int>(blockIdx.x % tiles_k) * 64;
-  f32x4_t acc[4] = {};
-  for (int t0 = 0; t0 < tokens; t0 += 32) {
-    for (int e = threadIdx.x; e < 64 * 32; e += kThreads) {
-      const int t = t0 + e / 64, c = e & 63;
-      uint16_t d = 0, x = 0;
-      if (t < tokens && n0 + c < n) d = dy[static_cast<int64_t>(t) * n + n0 + c];
-      if (t < tokens && k0 + c < k) {
-        const float v = __builtin_amdgcn_cvt_f32_fp8(q[static_cast<int64_t>(t) * kcols + k0 + c], 0);
-        x = static_cast<uint16_t>(pack_bf16x2(v * scale_value(scale[static_cast<int64_t>(t) * kscales + (k0 + c) / kBlock]), 0.0f));
-      }
-      td[c][e / 64] = d;
-      tx[c][e / 64] = x;
-    }
-    __syncthreads();
-    const bf16x8_t d = *reinterpret_cast<const bf16x8_t*>(&td[16 * wave + r][8 * g]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(*reinterpret_cast<const bf16x8_t*>(&tx[16 * i + r][8 * g]), d, acc[i], 0, 0, 0);
-    __syncthreads();
+// -------------------------------------------------------------- weight gradient
+//
+// dw[n, k] = sum over t of dy[t, n] * x[t, k].  The sum runs over rows, and the
+// scales of x differ from row to row, so they cannot wait until after the
+// product as in matmul_fp8: the codes are widened to bf16 with their scale on
+// the way into LDS (exact: 4 significant bits times a power of two), once per
+// workgroup, and v_mfma_f32_16x16x32_bf16 multiplies them with dy as it is.
+// x is the first operand, so a lane ends with four consecutive k of one row.
+//
+// Both operands lie in LDS as in memory, rows of t; the transposing LDS read
+// gives a lane four consecutive t of its column.  Sixteen lanes read four rows
+// of 16 columns (32 bytes, a "granule"), so a row's granules are permuted by
+// three bits of t that differ among the eight rows read in one cycle.
+constexpr int kTokens = 64;                     // rows of t per step: two products of 32
+
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+
+template <int COLS>
+struct TokenTile {
+  static constexpr int kRow = 2 * COLS, kBytes = kTokens * kRow;
+  static __device__ __forceinline__ int swizzle(int t) {
+    return COLS >= 128 ? (t & 3) | (t >> 1 & 4) : (t >> 1 & 1) | (t >> 2 & 2);
   }
+  // Byte of granule s of row t.
+  static __device__ __forceinline__ int at(int t, int s) { return t * kRow + 32 * (s ^ swizzle(t)); }
+};
+
+// Columns 16 i + 0..15 (from the granule s0 of the lane's offset on) of 32 rows:
+// lane l gets column l % 16 and rows 8 (l / 16) + 0..7 of them.  lane_off is
+// that of read_offset(s0); `chunk` the 32 rows.
+template <int COLS>
+__device__ __forceinline__ int read_offset(int lane, int s0) {
+  return TokenTile<COLS>::at(8 * (lane >> 4) + ((lane & 15) >> 2), s0) + 8 * (lane & 3);
+}
+
+template <int COLS>
+__device__ __forceinline__ bf16x8_t read_columns(const uint8_t* tile, int lane_off, int i, int chunk) {
+  typedef __attribute__((address_space(3))) i16x4_t* lds_ptr;
+  const uint8_t* p = tile + (lane_off ^ (32 * i)) + 32 * chunk * TokenTile<COLS>::kRow;
+  const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p));
+  const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 4 * TokenTile<COLS>::kRow));
+  const auto v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(bf16x8_t, v);
+}
+
+// How rows of dy are read: in 8-column pieces that lie inside a row or outside
+// it, in pieces of rows of any length from 8, or element by element.
+enum DyRows { kDyWhole, kDyOdd, kDyShort };
+
+// v >> 16 * e, e in 0..7: the elements from e on, first.
+__device__ __forceinline__ uint4 drop_elements(const uint4 v, int e) {
+  unsigned w[5] = {v.x, v.y, v.z, v.w, 0};
+  if (e & 4) w[0] = w[2], w[1] = w[3], w[2] = w[3] = 0;
+  if (e & 2) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = 0;
+  const unsigned bits = 16 * (e & 1);
+  return make_uint4(__builtin_amdgcn_alignbit(w[1], w[0], bits), __builtin_amdgcn_alignbit(w[2], w[1], bits),
+                    __builtin_amdgcn_alignbit(w[3], w[2], bits), __builtin_amdgcn_alignbit(w[4], w[3], bits));
+}
+
+// A step's part of dy that a thread moves: N pieces of 8 columns.  The loads
+// have no branch and nothing waits for them before store(): rows past the last
+// are read from the last and cleared on the way into LDS, pieces that cross the
+// end of a row start 8 elements before it and drop what precedes them, and
+// pieces past it hold anything (they reach only columns of the tile that are
+// not stored).
+template <int COLS, int THREADS, DyRows ROWS>
+struct DyPart {
+  static constexpr int N = kTokens * COLS / 8 / THREADS;
+  uint4 v[N];
+  __device__ __forceinline__ void load(unsigned thread, const uint16_t* dy, int t0, int tokens, int n0, int n) {
+    const uint16_t* base = dy + static_cast<int64_t>(t0) * n;
+    const uint8_t* bytes = uniform(reinterpret_cast<const uint8_t*>(base));
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int row = n0 + 16 * wave + r, col = k0 + 16 * i + 4 * g + c;
-      if (row < n && col < k) {
-        float* p = dw + static_cast<int64_t>(row) * k + col;
-        *p = accumulate ? *p + acc[i][c] : acc[i][c];
+    for (int i = 0; i < N; ++i) {
+      const unsigned p = i * THREADS + thread;
+      const int c = n0 + 8 * (p % (COLS / 8)), t = min(static_cast<int>(p / (COLS / 8)), tokens - 1 - t0);
+      if constexpr (ROWS == kDyShort) {
+        v[i] = load_chunk<false>(base + static_cast<int64_t>(t) * n, c, n);
+      } else {
+        const unsigned off = 2 * (static_cast<unsigned>(t) * n + min(c, n - 8));
+        v[i] = load16_at(bytes, off);                         // rows of odd length start at any element
       }
     }
+  }
+  __device__ __forceinline__ void store(unsigned thread, uint8_t* tile, int t0, int tokens, int n0, int n) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const unsigned p = i * THREADS + thread;
+      const int t = p / (COLS / 8), c = p % (COLS / 8);
+      uint4 u = v[i];
+      if constexpr (ROWS == kDyOdd) u = drop_elements(u, min(max(n0 + 8 * c - (n - 8), 0), 7));
+      const unsigned keep = t < tokens - t0 ? ~0u : 0u;
+      u = make_uint4(u.x & keep, u.y & keep, u.z & keep, u.w & keep);
+      *reinterpret_cast<uint4*>(tile + TokenTile<COLS>::at(t, c >> 1) + 16 * (c & 1)) = u;
+    }
+  }
+};
+
+// The same of x: N pieces of 16 codes with their scale, widened in store().
+template <int COLS, int THREADS>
+struct XPart {
+  static constexpr int N = kTokens * COLS / 16 / THREADS;
+  uint4 v[N];
+  unsigned byte[N];
+  __device__ __forceinline__ void load(unsigned thread, const uint8_t* q, const uint8_t* scale, int t0, int tokens, int k0,
+                                       int kcols, int kscales) {
+    const uint8_t* codes = uniform(q + static_cast<int64_t>(t0) * kcols);
+    const uint8_t* bytes = uniform(scale + static_cast<int64_t>(t0) * kscales);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const unsigned p = i * THREADS + thread, c = min(k0 + 16 * (p % (COLS / 16)), kcols - 16u);
+      const unsigned t = min(static_cast<int>(p / (COLS / 16)), tokens - 1 - t0);
+      // products apart from their sums: as one 64-bit multiply-add the compiler
+      // let the undefined upper half wait for loads in flight
+      int row_q = t * kcols, row_s = t * kscales;
+      opaque(row_q);
+      opaque(row_s);
+      v[i] = load16_at(codes, row_q + c);
+      byte[i] = load1_at(bytes, row_s + c / kBlock);
+    }
+  }
+  __device__ __forceinline__ void store(unsigned thread, uint8_t* tile, int t0, int tokens) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const unsigned p = i * THREADS + thread;
+      const int t = p / (COLS / 16), s = p % (COLS / 16);
+      const bool in = t < tokens - t0;
+      const float f = __builtin_bit_cast(float, in ? byte[i] << 23 : kScaleOne << 23);   // its exponent counts
+      const unsigned keep = in ? ~0u : 0u, nan = in && byte[i] == kScaleNan ? 0x7F7F7F7Fu : 0u;
+      const unsigned u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      unsigned w[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int code = static_cast<int>((u[j] & keep) | nan);
+        w[2 * j] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code, f, false));
+        w[2 * j + 1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code, f, true));
+      }
+      uint4* to = reinterpret_cast<uint4*>(tile + TokenTile<COLS>::at(t, s));
+      to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+};
+
+template <int KT, int NT>
+__device__ __forceinline__ void multiply(const bf16x8_t (&x)[KT], const bf16x8_t (&d)[NT], f32x4_t (&acc)[KT][NT]) {
+  __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+  for (int i = 0; i < KT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], d[j], acc[i][j], 0, 0, 0);
+  __builtin_amdgcn_s_setprio(0);
+}
+
+// Four consecutive k of a row of dw.  k may be odd: any 4-byte alignment.
+__device__ __forceinline__ void store_gradient(float* row, int col, int k, f32x4_t v, bool add) {
+  if (col + 4 <= k) {
+    if (add) {
+      f32x4_t o;
+      __builtin_memcpy(&o, row + col, 16);
+      v += o;
+    }
+    __builtin_memcpy(row + col, &v, 16);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 3; ++c)
+      if (col + c < k) row[col + c] = add ? row[col + c] + v[c] : v[c];
+  }
+}
+
+struct WgradArgs {
+  const uint16_t* dy;
+  const uint8_t *q, *scale;
+  int tokens, n, k, kcols, kscales;
+  float* dw;
+  int add;                                       // add to dw
+  int splits, split_steps;                       // partial sums over runs of split_steps steps, at dw + split * n * k
+};
+
+// Tiles of BN = 16 NT WN rows by BK = 16 KT WK columns of dw, two steps in LDS,
+// the next one's global loads in registers.
+template <int KT, int NT, int WK, int WN, DyRows ROWS>
+__global__ __launch_bounds__(64 * WK * WN) void wgrad_tiles_kernel(const WgradArgs p) {
+  constexpr int BK = 16 * KT * WK, BN = 16 * NT * WN, kThreads = 64 * WK * WN;
+  using X = TokenTile<BK>;
+  using D = TokenTile<BN>;
+  __shared__ __align__(256) uint8_t lds[2 * (X::kBytes + D::kBytes)];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles_n = (p.n + BN - 1) / BN, tiles_k = (p.k + BK - 1) / BK;
+  int tile_n, tile_k;
+  tile_of_block(tiles_n, tiles_k, tile_n, tile_k);
+  const int n0 = tile_n * BN, k0 = tile_k * BK;
+  const int first = blockIdx.y * p.split_steps * kTokens;
+  const int last = min(p.tokens, first + p.split_steps * kTokens);
+  const int wk = wave % WK, wn = wave / WK;
+  const int off_x = read_offset<BK>(lane, KT * wk), off_d = read_offset<BN>(lane, NT * wn);
+  XPart<BK, kThreads> x;
+  DyPart<BN, kThreads, ROWS> d;
+  f32x4_t acc[KT][NT] = {};
+  x.load(threadIdx.x, p.q, p.scale, first, last, k0, p.kcols, p.kscales);
+  d.load(threadIdx.x, p.dy, first, last, n0, p.n);
+  int buf = 0;
+  for (int t0 = first; t0 < last; t0 += kTokens, buf ^= 1) {
+    uint8_t* tx = lds + buf * X::kBytes;
+    uint8_t* td = lds + 2 * X::kBytes + buf * D::kBytes;
+    x.store(threadIdx.x, tx, t0, last);
+    d.store(threadIdx.x, td, t0, last, n0, p.n);
+    if (t0 + kTokens < last) {
+      x.load(threadIdx.x, p.q, p.scale, t0 + kTokens, last, k0, p.kcols, p.kscales);
+      d.load(threadIdx.x, p.dy, t0 + kTokens, last, n0, p.n);
+    }
+    reads_done_and_meet();
+#pragma unroll
+    for (int c = 0; c < kTokens / 32; ++c) {
+      bf16x8_t fx[KT], fd[NT];
+#pragma unroll
+      for (int i = 0; i < KT; ++i) fx[i] = read_columns<BK>(tx, off_x, i, c);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fd[j] = read_columns<BN>(td, off_d, j, c);
+      multiply(fx, fd, acc);
+    }
+  }
+  float* out = p.dw + static_cast<int64_t>(blockIdx.y) * p.n * p.k;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int row = n0 + 16 * (NT * wn + j) + (lane & 15);
+    if (row >= p.n) continue;
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+      store_gradient(out + static_cast<int64_t>(row) * p.k, k0 + 16 * (KT * wk + i) + 4 * (lane >> 4), p.k, acc[i][j],
+                     p.add != 0);
+  }
+}
+
+// The large gradient: 256 x 256 tiles, two groups of four wavefronts that take
+// turns as in matmul_turns_kernel: while one group multiplies 32 rows of t, the
+// other reads its fragments of 32.  A step of 64 rows has four phases, M0, C0,
+// M1, C1, the second group one behind.  The thread's part of step s + 1 goes
+// from registers to LDS in M0 (dy) and M1 (x, widened) of step s, when both
+// groups are done with step s - 1 in that buffer, and its loads for step s + 2
+// follow at once: four phases until they are used.
+template <DyRows ROWS>
+__global__ __launch_bounds__(512) void wgrad_turns_kernel(const WgradArgs p) {
+  constexpr int KT = 8, NT = 4, B = 256, kThreads = 512;
+  using Tile = TokenTile<B>;
+  __shared__ __align__(256) uint8_t lds[4 * Tile::kBytes];           // x, x, dy, dy
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles_n = (p.n + B - 1) / B, tiles_k = (p.k + B - 1) / B;
+  int tile_n, tile_k;
+  tile_of_block(tiles_n, tiles_k, tile_n, tile_k);
+  const int n0 = tile_n * B, k0 = tile_k * B;
+  const int wk = wave & 1, wn = wave >> 1;
+  int off_x = read_offset<B>(lane, KT * wk), off_d = read_offset<B>(lane, NT * wn), thread = threadIdx.x;
+  const int steps = (p.tokens + kTokens - 1) / kTokens;
+  XPart<B, kThreads> x;
+  DyPart<B, kThreads, ROWS> d;
+  f32x4_t acc[KT][NT] = {};
+  // past the last step the last one is read again, into a buffer nobody reads
+  auto load_x = [&](int s) { x.load(thread, p.q, p.scale, min(s, steps - 1) * kTokens, p.tokens, k0, p.kcols, p.kscales); };
+  auto load_d = [&](int s) { d.load(thread, p.dy, min(s, steps - 1) * kTokens, p.tokens, n0, p.n); };
+  auto store_x = [&](int s, int buf) { x.store(thread, lds + buf * Tile::kBytes, min(s, steps - 1) * kTokens, p.tokens); };
+  auto store_d = [&](int s, int buf) {
+    d.store(thread, lds + (2 + buf) * Tile::kBytes, min(s, steps - 1) * kTokens, p.tokens, n0, p.n);
+  };
+  load_x(0);
+  load_d(0);
+  store_x(0, 0);
+  store_d(0, 0);
+  load_d(1);
+  load_x(1);
+  reads_done_and_meet();
+  auto run = [&](auto group) {
+    if constexpr (group.value) meet();
+    for (int s = 0, buf = 0; s < steps; ++s, buf ^= 1) {
+      const uint8_t* tx = lds + buf * Tile::kBytes;
+      const uint8_t* td = lds + (2 + buf) * Tile::kBytes;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        // what follows from these is computed anew each time: kept in registers it spilled
+        opaque(off_x);
+        opaque(off_d);
+        opaque(thread);
+        if (c == 0) {
+          store_d(s + 1, buf ^ 1);
+          fence();
+          load_d(s + 2);
+        } else {
+          store_x(s + 1, buf ^ 1);
+          fence();
+          load_x(s + 2);
+        }
+        fence();
+        bf16x8_t fx[KT], fd[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) fd[j] = read_columns<B>(td, off_d, j, c);
+#pragma unroll
+        for (int i = 0; i < KT; ++i) fx[i] = read_columns<B>(tx, off_x, i, c);
+        reads_done_and_meet();
+        multiply(fx, fd, acc);
+        meet();
+      }
+    }
+    if constexpr (!group.value) meet();
+  };
+  if (wave >= 4)
+    run(std::true_type{});
+  else
+    run(std::false_type{});
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int row = n0 + 16 * (NT * wn + j) + (lane & 15);
+    if (row >= p.n) continue;
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+      store_gradient(p.dw + static_cast<int64_t>(row) * p.k, k0 + 16 * (KT * wk + i) + 4 * (lane >> 4), p.k, acc[i][j],
+                     p.add != 0);
+  }
+}
+
+// dw = (dw +) the partial sums, in order.
+__global__ __launch_bounds__(256) void wgrad_sum_kernel(const float* __restrict__ partial, int64_t count, int splits,
+                                                        float* __restrict__ dw, int add) {
+  const int64_t i = 4 * (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x);
+  if (i >= count) return;
+  if (i + 4 <= count) {
+    f32x4_t v = {};
+    for (int s = 0; s < splits; ++s) {
+      f32x4_t o;
+      __builtin_memcpy(&o, partial + s * count + i, 16);
+      v += o;
+    }
+    if (add) v += *reinterpret_cast<const f32x4_t*>(dw + i);
+    *reinterpret_cast<f32x4_t*>(dw + i) = v;
+  } else {
+    for (int64_t j = i; j < count; ++j) {
+      float v = 0.0f;
+      for (int s = 0; s < splits; ++s) v += partial[s * count + j];
+      dw[j] = add ? v + dw[j] : v;
+    }
+  }
 }
 
 struct MatmulArgs {
@@ -609,6 +931,63 @@ void launch_matmul(const MatmulArgs& p, hipStream_t stream) {
     launch_big(p, stream);
 }
 
+template <int KT, int NT, int WK, int WN>
+void launch_wgrad_tiles(const WgradArgs& p, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(tiles_of(p.n, p.k, 16 * NT * WN, 16 * KT * WK)), p.splits), wg(64 * WK * WN);
+  if (p.n % 8 == 0)
+    hipLaunchKernelGGL((wgrad_tiles_kernel<KT, NT, WK, WN, kDyWhole>), grid, wg, 0, stream, p);
+  else if (p.n >= 8)
+    hipLaunchKernelGGL((wgrad_tiles_kernel<KT, NT, WK, WN, kDyOdd>), grid, wg, 0, stream, p);
+  else
+    hipLaunchKernelGGL((wgrad_tiles_kernel<KT, NT, WK, WN, kDyShort>), grid, wg, 0, stream, p);
+}
+
+void launch_wgrad_turns(const WgradArgs& p, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(tiles_of(p.n, p.k, 256, 256)));
+  if (p.n % 8 == 0)
+    hipLaunchKernelGGL(wgrad_turns_kernel<kDyWhole>, grid, dim3(512), 0, stream, p);
+  else
+    hipLaunchKernelGGL(wgrad_turns_kernel<kDyOdd>, grid, dim3(512), 0, stream, p);
+}
+
+// Runs of steps whose partial sums go through the workspace: where even 64 x 64
+// tiles leave most CUs without work and there are many tokens.
+int wgrad_splits(int64_t tokens, int64_t n, int64_t k) {
+  const int64_t tiles = tiles_of(n, k, 64, 64), steps = (tokens + kTokens - 1) / kTokens;
+  return static_cast<int>(std::max<int64_t>(1, std::min(512 / tiles, steps / 4)));
+}
+
+void launch_wgrad(const WgradArgs& args, float* workspace, hipStream_t stream) {
+  WgradArgs p = args;
+  const int steps = (p.tokens + kTokens - 1) / kTokens;
+  p.splits = 1;
+  p.split_steps = steps;
+#ifdef FORCEW
+  switch (FORCEW) {
+    case 0: launch_wgrad_turns(p, stream); return;
+    case 1: launch_wgrad_tiles<4, 4, 2, 2>(p, stream); return;
+    case 2: launch_wgrad_tiles<2, 2, 2, 2>(p, stream); return;
+  }
+#endif
+  const int splits = wgrad_splits(p.tokens, p.n, p.k);
+  if (splits > 1) {
+    p.split_steps = (steps + splits - 1) / splits;
+    p.splits = (steps + p.split_steps - 1) / p.split_steps;
+    p.dw = workspace;
+    p.add = 0;
+    launch_wgrad_tiles<2, 2, 2, 2>(p, stream);
+    const int64_t count = static_cast<int64_t>(p.n) * p.k;
+    hipLaunchKernelGGL(wgrad_sum_kernel, dim3(static_cast<unsigned>((count + 1023) / 1024)), dim3(256), 0, stream,
+                       workspace, count, p.splits, args.dw, args.add);
+  } else if (tiles_of(p.n, p.k, 64, 64) <= 1024) {
+    launch_wgrad_tiles<2, 2, 2, 2>(p, stream);
+  } else if (tiles_of(p.n, p.k, 256, 256) < 192) {
+    launch_wgrad_tiles<4, 4, 2, 2>(p, stream);
+  } else {
+    launch_wgrad_turns(p, stream);
+  }
+}
+
 }  // namespace
 
 extern "C" {
@@ -634,7 +1013,11 @@ taco_status_t taco_matmul_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_
   return launched();
 }
 
-size_t taco_wgrad_fp8_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t taco_wgrad_fp8_workspace_bytes(int64_t tokens, int64_t n, int64_t k) {
+  if (!matrix_ok(tokens, n) || !matrix_ok(tokens, k) || !matrix_ok(n, k)) return 0;
+  const int splits = wgrad_splits(tokens, n, k);
+  return splits > 1 ? static_cast<size_t>(4 * n * k) * splits : 0;
+}
 
 taco_status_t taco_wgrad_fp8(const void* dy_bf16, const uint8_t* q, const uint8_t* scale, int64_t tokens, int64_t n,
                              int64_t k, float* dw, int32_t accumulate, void* workspace, size_t workspace_bytes,
@@ -650,10 +1033,9 @@ taco_status_t taco_wgrad_fp8(const void* dy_bf16, const uint8_t* q, const uint8_
               {{dy_bf16, static_cast<size_t>(2 * tokens * n)}, {q, static_cast<size_t>(tokens * kcols)},
                {scale, static_cast<size_t>(tokens * kscales)}}))
     return TACO_ERR_ALIAS;
-  const int64_t tiles = (n + 63) / 64 * ((k + 63) / 64);
-  hipLaunchKernelGGL(wgrad_fp8_kernel, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), 0, stream,
-                     static_cast<const uint16_t*>(dy_bf16), q, scale, static_cast<int>(tokens), static_cast<int>(n),
-                     static_cast<int>(k), static_cast<int>(kcols), static_cast<int>(kscales), dw, accumulate);
+  launch_wgrad({static_cast<const uint16_t*>(dy_bf16), q, scale, static_cast<int>(tokens), static_cast<int>(n),
+                static_cast<int>(k), static_cast<int>(kcols), static_cast<int>(kscales), dw, accumulate, 1, 0},
+               static_cast<float*>(workspace), stream);
   return launched();
 }
 
