@@ -625,6 +625,21 @@ struct DyPart {
   }
 };
 
+// 16 codes with their scale as bf16.  The conversion takes the exponent of its
+// fp32 scale; byte 255 gives NaN.
+__device__ __forceinline__ void widen16(const uint4 codes, unsigned byte, uint4* to) {
+  const float f = __builtin_bit_cast(float, byte << 23);
+  const unsigned u[4] = {codes.x, codes.y, codes.z, codes.w};
+  unsigned w[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    w[2 * j] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(static_cast<int>(u[j]), f, false));
+    w[2 * j + 1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(static_cast<int>(u[j]), f, true));
+  }
+  to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
 // The same of x: N pieces of 16 codes with their scale, widened in store().
 template <int COLS, int THREADS>
 struct XPart {
@@ -653,31 +668,24 @@ struct XPart {
     for (int i = 0; i < N; ++i) {
       const unsigned p = i * THREADS + thread;
       const int t = p / (COLS / 16), s = p % (COLS / 16);
-      const bool in = t < tokens - t0;
-      const float f = __builtin_bit_cast(float, in ? byte[i] << 23 : kScaleOne << 23);   // its exponent counts
-      const unsigned keep = in ? ~0u : 0u, nan = in && byte[i] == kScaleNan ? 0x7F7F7F7Fu : 0u;
-      const unsigned u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      unsigned w[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int code = static_cast<int>((u[j] & keep) | nan);
-        w[2 * j] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code, f, false));
-        w[2 * j + 1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code, f, true));
-      }
-      uint4* to = reinterpret_cast<uint4*>(tile + TokenTile<COLS>::at(t, s));
-      to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      const unsigned keep = t < tokens - t0 ? ~0u : 0u;
+      widen16(make_uint4(v[i].x & keep, v[i].y & keep, v[i].z & keep, v[i].w & keep),
+              t < tokens - t0 ? byte[i] : kScaleOne, reinterpret_cast<uint4*>(tile + TokenTile<COLS>::at(t, s)));
     }
   }
 };
 
-template <int KT, int NT>
-__device__ __forceinline__ void multiply(const bf16x8_t (&x)[KT], const bf16x8_t (&d)[NT], f32x4_t (&acc)[KT][NT]) {
+// between(i) runs after the NT products of x[i], in the shadow of the matrix pipe.
+template <int KT, int NT, typename F>
+__device__ __forceinline__ void multiply(const bf16x8_t (&x)[KT], const bf16x8_t (&d)[NT], f32x4_t (&acc)[KT][NT],
+                                         F between) {
   __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-  for (int i = 0; i < KT; ++i)
+  for (int i = 0; i < KT; ++i) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], d[j], acc[i][j], 0, 0, 0);
+    between(i);
+  }
   __builtin_amdgcn_s_setprio(0);
 }
 
@@ -747,7 +755,7 @@ __global__ __launch_bounds__(64 * WK * WN) void wgrad_tiles_kernel(const WgradAr
       for (int i = 0; i < KT; ++i) fx[i] = read_columns<BK>(tx, off_x, i, c);
 #pragma unroll
       for (int j = 0; j < NT; ++j) fd[j] = read_columns<BN>(td, off_d, j, c);
-      multiply(fx, fd, acc);
+      multiply(fx, fd, acc, [](int) {});
     }
   }
   float* out = p.dw + static_cast<int64_t>(blockIdx.y) * p.n * p.k;
@@ -766,77 +774,131 @@ __global__ __launch_bounds__(64 * WK * WN) void wgrad_tiles_kernel(const WgradAr
 // turns as in matmul_turns_kernel: while one group multiplies 32 rows of t, the
 // other reads its fragments of 32.  A step of 64 rows has four phases, M0, C0,
 // M1, C1, the second group one behind.  The thread's part of step s + 1 goes
-// from registers to LDS in M0 (dy) and M1 (x, widened) of step s, when both
-// groups are done with step s - 1 in that buffer, and its loads for step s + 2
-// follow at once: four phases until they are used.
+// from registers to LDS in C0 of step s, between the matrix instructions, when
+// both groups are done with step s - 1 in that buffer; both have waited for
+// their writes by the end of M1, before anybody reads step s + 1.  The loads
+// for step s + 2 follow at once: four phases until they are used.
+//
+// A phase lasts as long as the longer of the two groups' work, so the M phases
+// hold nothing but the reads, and whole steps need no check of rows and one
+// offset per operand (a thread's pieces are a fixed number of rows apart); the
+// rows that are left over follow as one step of their own, without turns.
 template <DyRows ROWS>
 __global__ __launch_bounds__(512) void wgrad_turns_kernel(const WgradArgs p) {
   constexpr int KT = 8, NT = 4, B = 256, kThreads = 512;
   using Tile = TokenTile<B>;
+  using D = DyPart<B, kThreads, ROWS>;
+  using X = XPart<B, kThreads>;
+  constexpr int kRowsD = kTokens / D::N, kRowsX = kTokens / X::N;     // between a thread's pieces
+  static_assert(kRowsD % 16 == 0 && kRowsX % 16 == 0, "rows that far apart have the same swizzle");
   __shared__ __align__(256) uint8_t lds[4 * Tile::kBytes];           // x, x, dy, dy
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, thread = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles_n = (p.n + B - 1) / B, tiles_k = (p.k + B - 1) / B;
   int tile_n, tile_k;
   tile_of_block(tiles_n, tiles_k, tile_n, tile_k);
   const int n0 = tile_n * B, k0 = tile_k * B;
   const int wk = wave & 1, wn = wave >> 1;
-  int off_x = read_offset<B>(lane, KT * wk), off_d = read_offset<B>(lane, NT * wn), thread = threadIdx.x;
-  const int steps = (p.tokens + kTokens - 1) / kTokens;
-  XPart<B, kThreads> x;
-  DyPart<B, kThreads, ROWS> d;
-  f32x4_t acc[KT][NT] = {};
+  int off_x = read_offset<B>(lane, KT * wk), off_d = read_offset<B>(lane, NT * wn);
+
+  const int col_d = n0 + 8 * (thread & 31), col_x = min(k0 + 16 * (thread & 15), p.kcols - 16);
+  const unsigned from_d = 2 * ((thread >> 5) * p.n + min(col_d, p.n - 8));
+  const unsigned from_q = (thread >> 4) * p.kcols + col_x, from_s = (thread >> 4) * p.kscales + col_x / kBlock;
+  const int to_d = Tile::at(thread >> 5, (thread & 31) >> 1) + 16 * (thread & 1);
+  const int to_x = Tile::at(thread >> 4, thread & 15);
+  const int drop = min(max(col_d - (p.n - 8), 0), 7);
+  const int steps = p.tokens / kTokens;
+  D d;
+  X x;
   // past the last step the last one is read again, into a buffer nobody reads
-  auto load_x = [&](int s) { x.load(thread, p.q, p.scale, min(s, steps - 1) * kTokens, p.tokens, k0, p.kcols, p.kscales); };
-  auto load_d = [&](int s) { d.load(thread, p.dy, min(s, steps - 1) * kTokens, p.tokens, n0, p.n); };
-  auto store_x = [&](int s, int buf) { x.store(thread, lds + buf * Tile::kBytes, min(s, steps - 1) * kTokens, p.tokens); };
-  auto store_d = [&](int s, int buf) {
-    d.store(thread, lds + (2 + buf) * Tile::kBytes, min(s, steps - 1) * kTokens, p.tokens, n0, p.n);
+  auto load_d = [&](int s, int i) {
+    const int64_t t = static_cast<int64_t>(min(s, steps - 1)) * kTokens + i * kRowsD;
+    d.v[i] = load16_at(uniform(reinterpret_cast<const uint8_t*>(p.dy + t * p.n)), from_d);
   };
-  load_x(0);
-  load_d(0);
-  store_x(0, 0);
-  store_d(0, 0);
-  load_d(1);
-  load_x(1);
-  reads_done_and_meet();
+  auto load_x = [&](int s, int i) {
+    const int64_t t = static_cast<int64_t>(min(s, steps - 1)) * kTokens + i * kRowsX;
+    x.v[i] = load16_at(uniform(p.q + t * p.kcols), from_q);
+    x.byte[i] = load1_at(uniform(p.scale + t * p.kscales), from_s);
+  };
+  auto store_d = [&](int buf, int i) {
+    *reinterpret_cast<uint4*>(lds + (2 + buf) * Tile::kBytes + to_d + i * kRowsD * Tile::kRow) =
+        ROWS == kDyOdd ? drop_elements(d.v[i], drop) : d.v[i];
+  };
+  auto store_x = [&](int buf, int i) {
+    widen16(x.v[i], x.byte[i], reinterpret_cast<uint4*>(lds + buf * Tile::kBytes + to_x + i * kRowsX * Tile::kRow));
+  };
+  f32x4_t acc[KT][NT] = {};
+  auto read = [&](int buf, int c, bf16x8_t (&fx)[KT], bf16x8_t (&fd)[NT]) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) fd[j] = read_columns<B>(lds + (2 + buf) * Tile::kBytes, off_d, j, c);
+#pragma unroll
+    for (int i = 0; i < KT; ++i) fx[i] = read_columns<B>(lds + buf * Tile::kBytes, off_x, i, c);
+  };
   auto run = [&](auto group) {
     if constexpr (group.value) meet();
     for (int s = 0, buf = 0; s < steps; ++s, buf ^= 1) {
-      const uint8_t* tx = lds + buf * Tile::kBytes;
-      const uint8_t* td = lds + (2 + buf) * Tile::kBytes;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        // what follows from these is computed anew each time: kept in registers it spilled
-        opaque(off_x);
+        opaque(off_x);       // the permuted addresses are computed anew: kept in registers they spilled
         opaque(off_d);
-        opaque(thread);
-        if (c == 0) {
-          store_d(s + 1, buf ^ 1);
-          fence();
-          load_d(s + 2);
-        } else {
-          store_x(s + 1, buf ^ 1);
-          fence();
-          load_x(s + 2);
-        }
-        fence();
         bf16x8_t fx[KT], fd[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) fd[j] = read_columns<B>(td, off_d, j, c);
-#pragma unroll
-        for (int i = 0; i < KT; ++i) fx[i] = read_columns<B>(tx, off_x, i, c);
+        read(buf, c, fx, fd);
         reads_done_and_meet();
-        multiply(fx, fd, acc);
+        multiply(fx, fd, acc, [&](int i) {
+          if (c != 0) return;
+          fence();
+          if (i < D::N) {
+            store_d(buf ^ 1, i);
+            fence();
+            load_d(s + 2, i);
+          } else if (i < D::N + X::N) {
+            store_x(buf ^ 1, i - D::N);
+            fence();
+            load_x(s + 2, i - D::N);
+          }
+          fence();
+        });
         meet();
       }
     }
     if constexpr (!group.value) meet();
   };
-  if (wave >= 4)
-    run(std::true_type{});
-  else
-    run(std::false_type{});
+  if (steps > 0) {
+#pragma unroll
+    for (int i = 0; i < D::N; ++i) load_d(0, i);
+#pragma unroll
+    for (int i = 0; i < X::N; ++i) load_x(0, i);
+#pragma unroll
+    for (int i = 0; i < D::N; ++i) {
+      store_d(0, i);
+      load_d(1, i);
+    }
+#pragma unroll
+    for (int i = 0; i < X::N; ++i) {
+      store_x(0, i);
+      load_x(1, i);
+    }
+    reads_done_and_meet();
+    if (wave >= 4)
+      run(std::true_type{});
+    else
+      run(std::false_type{});
+  }
+  const int t0 = steps * kTokens;
+  if (t0 < p.tokens) {
+    x.load(thread, p.q, p.scale, t0, p.tokens, k0, p.kcols, p.kscales);
+    d.load(thread, p.dy, t0, p.tokens, n0, p.n);
+    __syncthreads();
+    x.store(thread, lds, t0, p.tokens);
+    d.store(thread, lds + 2 * Tile::kBytes, t0, p.tokens, n0, p.n);
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      bf16x8_t fx[KT], fd[NT];
+      read(0, c, fx, fd);
+      multiply(fx, fd, acc, [](int) {});
+    }
+  }
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int row = n0 + 16 * (NT * wn + j) + (lane & 15);
