@@ -366,20 +366,21 @@ __global__ __launch_bounds__(64 * kFewWaves) void matmul_few_kernel(
 // The operands stream through a ring of nine 16 KiB units in LDS, four per
 // step in the order b's first halves, a's rows 0..127, a's rows 128..255, b's
 // second halves.  Unit u goes to slot u % 9 once unit u - 9 has been read by
-// both groups.  Each phase issues one unit, two copies per wavefront, so the
-// copies reach the memory pipeline evenly: with P1..P4 the first group's M1(k),
-// C1(k), M2(k), C2(k) and the second's C2(k - 1), M1(k), C1(k), M2(k), they are
-// units 4 k + 7..4 k + 10.  Before the barrier that frees a unit for reading,
-// every wavefront waits until only newer units are in flight: at the end of P2
-// unit 4 k + 3 is due and five are newer, at the end of P4 unit 4 k + 6 with
-// four newer.  Copies retire in issue order, so operations issued later only
-// make a wait stricter.
+// both groups: with P1..P4 the phases in which the first group is in M1(k),
+// C1(k), M2(k), C2(k) and the second in C2(k - 1), M1(k), C1(k), M2(k), unit
+// 4 k + 8 may be issued from P1 on and units 4 k + 9..11 from P3 on.  Either
+// group issues its copies in its own M1 and M2, where they do not hold up the
+// matrix instructions.  Before the barrier that frees a unit for reading, every
+// wavefront waits until only newer units are in flight: unit 4 k + 3 is due at
+// the end of P2 and unit 4 k + 6 at the end of P4, with five newer ones (ten
+// copies of a wavefront) each.  Copies retire in issue order, so operations
+// issued later only make a wait stricter.
 //
-// 8192 x 8192 x 8192: 400 us, 2.75 PFLOP/s; 8192 x 14336 x 3584: 350 us, 2.4.
+// 8192 x 8192 x 8192: 383 us, 2.87 PFLOP/s; 8192 x 14336 x 3584: 336 us, 2.51.
 // Without the loop's copies 8192^3 takes 324 us, without the LDS reads 321, the
 // copies alone 206: the two compete for LDS and the barriers cost the rest.
-// With one step in flight (two whole buffers) it took 435 us, with a step's
-// copies issued at once 425.
+// With one step in flight (two whole buffers) it took 435 us, with the copies
+// among the matrix instructions 390.
 constexpr int kBig = 256;                       // rows of either operand in a tile
 constexpr int kUnit = 128 * kBlock;             // bytes: 128 rows of 128 columns
 constexpr int kRing = 9;
@@ -441,7 +442,8 @@ __global__ __launch_bounds__(512) void matmul_turns_kernel(
     copy_unit(gb, off_b1, 1, 4);
     copy_unit(ga, off_a1, 1, 5);
     copy_unit(ga, off_a2, 1, 6);
-    copies_left<8>();
+    copy_unit(gb, off_b2, 1, 7);
+    copies_left<10>();
   } else {
     copies_left<2>();
   }
@@ -450,10 +452,7 @@ __global__ __launch_bounds__(512) void matmul_turns_kernel(
   auto run = [&](auto group) {
     constexpr bool kSecond = group.value;
     int slot = 0;                                  // of the step's first unit
-    if constexpr (kSecond) {
-      if (steps > 1) copy_unit(gb, off_b2, 1, 7);
-      meet();
-    }
+    if constexpr (kSecond) meet();
     // TAIL 0: steps that have two more after them, 1: the last but one, 2: the last.
     auto step = [&](int k, auto tail) {
       constexpr int TAIL = tail.value;
@@ -461,17 +460,21 @@ __global__ __launch_bounds__(512) void matmul_turns_kernel(
       const uint8_t* tb = lds + slot * kUnit + 64 * kBlock * wn;
       const uint8_t* ta = lds + slot_after(slot, wm < 2 ? 1 : 2) * kUnit + 64 * kBlock * (wm & 1);
       const uint8_t* tb2 = lds + slot_after(slot, 3) * kUnit + 64 * kBlock * wn;
-      auto p1_copy = [&](int at, int s) { copy_unit(gb, off_b2, at + 1, slot_after(s, 7)); };
-      auto p2_copy = [&] {
+      auto m1_copies = [&] {
         if constexpr (TAIL == 0) {
           if ((k & 3) == 0 && k + 4 < steps) copy_scales(k + 4);
           copy_unit(gb, off_b1, k + 2, slot_after(slot, 8));
         }
       };
-      auto p3_copy = [&] { if constexpr (TAIL == 0) copy_unit(ga, off_a1, k + 2, slot); };
-      auto p4_copy = [&] { if constexpr (TAIL == 0) copy_unit(ga, off_a2, k + 2, slot_after(slot, 1)); };
+      auto m2_copies = [&] {
+        if constexpr (TAIL == 0) {
+          copy_unit(ga, off_a1, k + 2, slot);
+          copy_unit(ga, off_a2, k + 2, slot_after(slot, 1));
+          copy_unit(gb, off_b2, k + 2, slot_after(slot, 2));
+        }
+      };
       auto p2_wait = [&] { copies_left<TAIL == 0 ? 10 : TAIL == 1 ? 8 : 0>(); };   // this step's last unit
-      auto p4_wait = [&] { copies_left<TAIL == 0 ? 8 : TAIL == 1 ? 2 : 0>(); };    // the next step's first three
+      auto p4_wait = [&] { copies_left<TAIL == 0 ? 10 : TAIL == 1 ? 2 : 0>(); };   // the next step's first three
       i32x8_t a[MT], b[NT / 2];
       int scale_a[MT];
 #pragma unroll
@@ -481,27 +484,17 @@ __global__ __launch_bounds__(512) void matmul_turns_kernel(
 #pragma unroll
       for (int j = 0; j < MT; ++j) scale_a[j] = scales[4 * (64 * wm + 16 * j + r)];
       const int scale_b = scales[1024 + 4 * wn];
-      if constexpr (kSecond) {
-        p2_copy();
-        p2_wait();
-      } else if constexpr (TAIL < 2) {
-        p1_copy(k, slot);
-      }
+      m1_copies();
+      if constexpr (kSecond) p2_wait();
       reads_done_and_meet();
-      if constexpr (kSecond) p3_copy(); else p2_copy();
       multiply(b, a, scale_b, scale_a, &acc[0][0]);
       if constexpr (!kSecond) p2_wait();
       meet();
 #pragma unroll
       for (int i = 0; i < NT / 2; ++i) b[i] = load_fragment(tb2 + 16 * kBlock * i, lane_off);
-      if constexpr (kSecond) {
-        p4_copy();
-        p4_wait();
-      } else {
-        p3_copy();
-      }
+      m2_copies();
+      if constexpr (kSecond) p4_wait();
       reads_done_and_meet();
-      if constexpr (!kSecond) p4_copy(); else if constexpr (TAIL == 0) p1_copy(k + 1, slot_after(slot, 4));
       multiply(b, a, scale_b, scale_a, &acc[NT / 2][0]);
       if constexpr (!kSecond) p4_wait();
       meet();
