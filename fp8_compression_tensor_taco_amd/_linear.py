@@ -13,7 +13,7 @@ import ctypes
 
 import torch
 
-from ._binding import _check, _on, _stream, _workspace, load
+from ._binding import _check, _on, _workspace, load
 
 BLOCK = 128
 
@@ -61,59 +61,77 @@ def fp8_scale_cols(cols: int) -> int:
     return -(-fp8_cols(cols) // (4 * BLOCK)) * 4
 
 
-def _input(t, name, dtype, shape=None, dims=2):
+def _input(t, name, dtype, dims=2):
     """The tensor as the kernels take it: on a GPU, contiguous, 16-byte aligned."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError("libtaco works on GPU tensors only (no CPU fallback)")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
-    if shape is not None and tuple(t.shape) != shape:
+    if not t.is_contiguous():
+        return t.contiguous()
+    return t if t.data_ptr() & 15 == 0 else t.clone()
+
+
+def _shaped(t, name, dtype, shape, device):
+    """The same, of a given shape and on the call's device."""
+    t = _input(t, name, dtype, len(shape))
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+    if t.device != device:
+        raise ValueError("all tensors must be on the same device")
+    return t
 
 
 def _output(t, name, dtype, shape, device):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+    if t is None:          # with strides: quicker than torch.empty, and small calls are bound by the host
+        return torch.empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype=dtype, device=device)
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
     return t
 
 
-def _same_device(*tensors):
-    for t in tensors[1:]:
-        if t is not None and t.device != tensors[0].device:
-            raise ValueError("all tensors must be on the same device")
-    return tensors[0].device
+def _current(device):
+    """Handle of the device's current stream; the library launches on the current device."""
+    if torch._C._cuda_getDevice() != device.index:
+        raise ValueError(f"the tensors are on {device}, the current device is {torch._C._cuda_getDevice()}")
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _scratch(device, nbytes, kind, handle):
-    """(pointer, bytes) of the binding's workspace; none where 0 bytes are needed."""
+def _scratch(workspace, device, nbytes, kind, handle):
+    """(pointer, bytes) of the given workspace, or of the binding's own; none where 0 bytes are needed."""
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.device != device:
+            raise ValueError(f"workspace must be contiguous and on {device}")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if nbytes == 0:
         return None, 0
     ws = _workspace(device, nbytes, kind, handle)
     return ws.data_ptr(), ws.numel()
 
 
+# Every call with a stream makes it current and calls itself: outputs, copies of
+# inputs and the launch then belong to that stream (see _binding._on).
+
 def quantize_rows(x: torch.Tensor, *, q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
     """Quantise bf16 [rows, cols] into the block format.
 
     Returns (q uint8 [rows, fp8_cols(cols)], scale uint8 [rows, fp8_scale_cols(cols)])."""
-    with _on(stream):
-        x = _input(x, "x", torch.bfloat16)
-        rows, cols = x.shape
-        dev = x.device
-        q = _output(q, "q", torch.uint8, (rows, fp8_cols(cols)), dev)
-        scale = _output(scale, "scale", torch.uint8, (rows, fp8_scale_cols(cols)), dev)
-        _check(_lib().taco_quantize_rows(x.data_ptr(), rows, cols, q.data_ptr(), scale.data_ptr(), _stream(dev, stream)))
-        return q, scale
+    if stream is not None:
+        with _on(stream):
+            return quantize_rows(x, q=q, scale=scale)
+    x = _input(x, "x", torch.bfloat16)
+    rows, cols = x.shape
+    dev = x.device
+    q = _output(q, "q", torch.uint8, (rows, fp8_cols(cols)), dev)
+    scale = _output(scale, "scale", torch.uint8, (rows, fp8_scale_cols(cols)), dev)
+    _check(_lib().taco_quantize_rows(x.data_ptr(), rows, cols, q.data_ptr(), scale.data_ptr(), _current(dev)))
+    return q, scale
 
 
 def quantize_weight(w: torch.Tensor, *, transposed: bool = True, q: torch.Tensor | None = None,
@@ -124,20 +142,22 @@ def quantize_weight(w: torch.Tensor, *, transposed: bool = True, q: torch.Tensor
     Returns (q, scale, qt, scale_t): the weight [rows, cols] and the same codes
     of its transpose [cols, rows], both in the weight format, for the forward
     product and the input's gradient.  transposed=False gives None for the last two."""
-    with _on(stream):
-        w = _input(w, "w", torch.bfloat16)
-        rows, cols = w.shape
-        dev = w.device
-        q = _output(q, "q", torch.uint8, (rows, fp8_cols(cols)), dev)
-        scale = _output(scale, "scale", torch.uint8, (fp8_cols(rows) // BLOCK, fp8_scale_cols(cols)), dev)
-        if transposed:
-            qt = _output(qt, "qt", torch.uint8, (cols, fp8_cols(rows)), dev)
-            scale_t = _output(scale_t, "scale_t", torch.uint8, (fp8_cols(cols) // BLOCK, fp8_scale_cols(rows)), dev)
-        elif qt is not None or scale_t is not None:
-            raise ValueError("qt and scale_t are outputs of transposed=True")
-        _check(_lib().taco_quantize_weight(w.data_ptr(), rows, cols, q.data_ptr(), scale.data_ptr(), _ptr(qt),
-                                           _ptr(scale_t), _stream(dev, stream)))
-        return q, scale, qt, scale_t
+    if stream is not None:
+        with _on(stream):
+            return quantize_weight(w, transposed=transposed, q=q, scale=scale, qt=qt, scale_t=scale_t)
+    w = _input(w, "w", torch.bfloat16)
+    rows, cols = w.shape
+    dev = w.device
+    q = _output(q, "q", torch.uint8, (rows, fp8_cols(cols)), dev)
+    scale = _output(scale, "scale", torch.uint8, (fp8_cols(rows) // BLOCK, fp8_scale_cols(cols)), dev)
+    if transposed:
+        qt = _output(qt, "qt", torch.uint8, (cols, fp8_cols(rows)), dev)
+        scale_t = _output(scale_t, "scale_t", torch.uint8, (fp8_cols(cols) // BLOCK, fp8_scale_cols(rows)), dev)
+    elif qt is not None or scale_t is not None:
+        raise ValueError("qt and scale_t are outputs of transposed=True")
+    _check(_lib().taco_quantize_weight(w.data_ptr(), rows, cols, q.data_ptr(), scale.data_ptr(), _ptr(qt),
+                                       _ptr(scale_t), _current(dev)))
+    return q, scale, qt, scale_t
 
 
 def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, *,
@@ -149,23 +169,25 @@ def rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, *
     Returns (z, rstd, q, scale): z = bf16(x + residual), the new residual
     stream (x itself without a residual); rstd fp32 [tokens]; and
     z * rstd * weight in the block format."""
-    with _on(stream):
-        x = _input(x, "x", torch.bfloat16)
-        tokens, hidden = x.shape
-        weight = _input(weight, "weight", torch.bfloat16, (hidden,), 1)
-        dev = _same_device(x, weight, residual)
-        if residual is not None:
-            residual = _input(residual, "residual", torch.bfloat16, (tokens, hidden))
-            z = _output(z, "z", torch.bfloat16, (tokens, hidden), dev)
-        elif z is not None:
-            raise ValueError("z is an output of the call with a residual")
-        rstd = _output(rstd, "rstd", torch.float32, (tokens,), dev)
-        q = _output(q, "q", torch.uint8, (tokens, fp8_cols(hidden)), dev)
-        scale = _output(scale, "scale", torch.uint8, (tokens, fp8_scale_cols(hidden)), dev)
-        _check(_lib().taco_rmsnorm_quantize(x.data_ptr(), _ptr(residual), weight.data_ptr(), tokens, hidden, eps,
-                                            _ptr(z), rstd.data_ptr(), q.data_ptr(), scale.data_ptr(),
-                                            _stream(dev, stream)))
-        return x if z is None else z, rstd, q, scale
+    if stream is not None:
+        with _on(stream):
+            return rmsnorm_quantize(x, weight, eps, residual=residual, z=z, rstd=rstd, q=q, scale=scale)
+    x = _input(x, "x", torch.bfloat16)
+    tokens, hidden = x.shape
+    dev = x.device
+    weight = _shaped(weight, "weight", torch.bfloat16, (hidden,), dev)
+    if residual is not None:
+        residual = _shaped(residual, "residual", torch.bfloat16, (tokens, hidden), dev)
+        z = _output(z, "z", torch.bfloat16, (tokens, hidden), dev)
+    elif z is not None:
+        raise ValueError("z is an output of the call with a residual")
+    rstd = _output(rstd, "rstd", torch.float32, (tokens,), dev)
+    q = _output(q, "q", torch.uint8, (tokens, fp8_cols(hidden)), dev)
+    scale = _output(scale, "scale", torch.uint8, (tokens, fp8_scale_cols(hidden)), dev)
+    _check(_lib().taco_rmsnorm_quantize(x.data_ptr(), _ptr(residual), weight.data_ptr(), tokens, hidden, eps,
+                                        _ptr(z), rstd.data_ptr(), q.data_ptr(), scale.data_ptr(),
+                                        _current(dev)))
+    return x if z is None else z, rstd, q, scale
 
 
 def rmsnorm_backward(dy: torch.Tensor, z: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, *,
@@ -175,31 +197,24 @@ def rmsnorm_backward(dy: torch.Tensor, z: torch.Tensor, rstd: torch.Tensor, weig
 
     dz is the gradient that reached z by the residual path.  Returns (dx bf16,
     the gradient of x and of the residual; dweight fp32 [hidden])."""
-    with _on(stream):
-        dy = _input(dy, "dy", torch.bfloat16)
-        tokens, hidden = dy.shape
-        z = _input(z, "z", torch.bfloat16, (tokens, hidden))
-        rstd = _input(rstd, "rstd", torch.float32, (tokens,), 1)
-        weight = _input(weight, "weight", torch.bfloat16, (hidden,), 1)
-        if dz is not None:
-            dz = _input(dz, "dz", torch.bfloat16, (tokens, hidden))
-        dev = _same_device(dy, z, rstd, weight, dz, workspace)
-        dx = _output(dx, "dx", torch.bfloat16, (tokens, hidden), dev)
-        dweight = _output(dweight, "dweight", torch.float32, (hidden,), dev)
-        lib, handle = _lib(), _stream(dev, stream)
-        if workspace is None:
-            ws = _scratch(dev, lib.taco_rmsnorm_backward_workspace_bytes(tokens, hidden), "rmsnorm_backward", handle)
-        else:
-            ws = _given(workspace)
-        _check(lib.taco_rmsnorm_backward(dy.data_ptr(), z.data_ptr(), rstd.data_ptr(), weight.data_ptr(), _ptr(dz),
-                                         tokens, hidden, dx.data_ptr(), dweight.data_ptr(), *ws, handle))
-        return dx, dweight
-
-
-def _given(workspace):
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if stream is not None:
+        with _on(stream):
+            return rmsnorm_backward(dy, z, rstd, weight, dz=dz, dx=dx, dweight=dweight, workspace=workspace)
+    dy = _input(dy, "dy", torch.bfloat16)
+    tokens, hidden = dy.shape
+    dev = dy.device
+    z = _shaped(z, "z", torch.bfloat16, (tokens, hidden), dev)
+    rstd = _shaped(rstd, "rstd", torch.float32, (tokens,), dev)
+    weight = _shaped(weight, "weight", torch.bfloat16, (hidden,), dev)
+    if dz is not None:
+        dz = _shaped(dz, "dz", torch.bfloat16, (tokens, hidden), dev)
+    dx = _output(dx, "dx", torch.bfloat16, (tokens, hidden), dev)
+    dweight = _output(dweight, "dweight", torch.float32, (hidden,), dev)
+    lib, handle = _lib(), _current(dev)
+    ws = _scratch(workspace, dev, lib.taco_rmsnorm_backward_workspace_bytes(tokens, hidden), "rmsnorm_backward", handle)
+    _check(lib.taco_rmsnorm_backward(dy.data_ptr(), z.data_ptr(), rstd.data_ptr(), weight.data_ptr(), _ptr(dz),
+                                     tokens, hidden, dx.data_ptr(), dweight.data_ptr(), *ws, handle))
+    return dx, dweight
 
 
 def matmul_fp8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Tensor, *,
@@ -208,24 +223,25 @@ def matmul_fp8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.T
 
     With a = x and b = w a linear layer's output; with a = dy and b the
     transposed weight, the gradient of its input."""
-    with _on(stream):
-        qa, qb = _input(qa, "qa", torch.uint8), _input(qb, "qb", torch.uint8)
-        (m, k), n = qa.shape, qb.shape[0]
-        if k == 0 or k % BLOCK or qb.shape[1] != k:
-            raise ValueError(f"qa and qb must have the same number of columns, a multiple of {BLOCK}: "
-                             f"got {k} and {qb.shape[1]}")
-        sa = _input(sa, "sa", torch.uint8, (m, fp8_scale_cols(k)))
-        sb = _input(sb, "sb", torch.uint8, (-(-n // BLOCK), fp8_scale_cols(k)))
-        dev = _same_device(qa, sa, qb, sb, workspace)
-        out = _output(out, "out", torch.bfloat16, (m, n), dev)
-        lib, handle = _lib(), _stream(dev, stream)
-        if workspace is None:
-            ws = _scratch(dev, lib.taco_matmul_fp8_workspace_bytes(m, n, k), "matmul_fp8", handle)
-        else:
-            ws = _given(workspace)
-        _check(lib.taco_matmul_fp8(qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), m, n, k,
-                                   out.data_ptr(), *ws, handle))
-        return out
+    if stream is not None:
+        with _on(stream):
+            return matmul_fp8(qa, sa, qb, sb, out=out, workspace=workspace)
+    qa, qb = _input(qa, "qa", torch.uint8), _input(qb, "qb", torch.uint8)
+    (m, k), n = qa.shape, qb.shape[0]
+    if k == 0 or k % BLOCK or qb.shape[1] != k:
+        raise ValueError(f"qa and qb must have the same number of columns, a multiple of {BLOCK}: "
+                         f"got {k} and {qb.shape[1]}")
+    dev = qa.device
+    sa = _shaped(sa, "sa", torch.uint8, (m, fp8_scale_cols(k)), dev)
+    sb = _shaped(sb, "sb", torch.uint8, (-(-n // BLOCK), fp8_scale_cols(k)), dev)
+    if qb.device != dev:
+        raise ValueError("all tensors must be on the same device")
+    out = _output(out, "out", torch.bfloat16, (m, n), dev)
+    lib, handle = _lib(), _current(dev)
+    ws = _scratch(workspace, dev, lib.taco_matmul_fp8_workspace_bytes(m, n, k), "matmul_fp8", handle)
+    _check(lib.taco_matmul_fp8(qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), m, n, k,
+                               out.data_ptr(), *ws, handle))
+    return out
 
 
 def wgrad_fp8(dy: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, cols: int, *, dw: torch.Tensor | None = None,
@@ -234,23 +250,22 @@ def wgrad_fp8(dy: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, cols: int,
 
     x is a linear layer's input as it was kept in 8 bits.  accumulate=True adds
     to dw, which must then be given."""
-    with _on(stream):
-        dy = _input(dy, "dy", torch.bfloat16)
-        tokens, n = dy.shape
-        q = _input(q, "q", torch.uint8, (tokens, fp8_cols(cols)))
-        scale = _input(scale, "scale", torch.uint8, (tokens, fp8_scale_cols(cols)))
-        if accumulate and dw is None:
-            raise ValueError("accumulate=True adds to dw: pass it")
-        dev = _same_device(dy, q, scale, workspace)
-        dw = _output(dw, "dw", torch.float32, (n, cols), dev)
-        lib, handle = _lib(), _stream(dev, stream)
-        if workspace is None:
-            ws = _scratch(dev, lib.taco_wgrad_fp8_workspace_bytes(tokens, n, cols), "wgrad_fp8", handle)
-        else:
-            ws = _given(workspace)
-        _check(lib.taco_wgrad_fp8(dy.data_ptr(), q.data_ptr(), scale.data_ptr(), tokens, n, cols, dw.data_ptr(),
-                                  int(bool(accumulate)), *ws, handle))
-        return dw
+    if stream is not None:
+        with _on(stream):
+            return wgrad_fp8(dy, q, scale, cols, dw=dw, accumulate=accumulate, workspace=workspace)
+    dy = _input(dy, "dy", torch.bfloat16)
+    tokens, n = dy.shape
+    dev = dy.device
+    q = _shaped(q, "q", torch.uint8, (tokens, fp8_cols(cols)), dev)
+    scale = _shaped(scale, "scale", torch.uint8, (tokens, fp8_scale_cols(cols)), dev)
+    if accumulate and dw is None:
+        raise ValueError("accumulate=True adds to dw: pass it")
+    dw = _output(dw, "dw", torch.float32, (n, cols), dev)
+    lib, handle = _lib(), _current(dev)
+    ws = _scratch(workspace, dev, lib.taco_wgrad_fp8_workspace_bytes(tokens, n, cols), "wgrad_fp8", handle)
+    _check(lib.taco_wgrad_fp8(dy.data_ptr(), q.data_ptr(), scale.data_ptr(), tokens, n, cols, dw.data_ptr(),
+                              int(bool(accumulate)), *ws, handle))
+    return dw
 
 
 def swiglu_quantize(gu: torch.Tensor, *, checkpoint: bool = True, hq: torch.Tensor | None = None,
@@ -260,23 +275,25 @@ def swiglu_quantize(gu: torch.Tensor, *, checkpoint: bool = True, hq: torch.Tens
 
     Returns (hq, hs, cq, cs): silu(gate) * up in the block format, and gate and
     up in 8 bits for swiglu_backward (checkpoint=False gives None for those)."""
-    with _on(stream):
-        gu = _input(gu, "gu", torch.bfloat16)
-        tokens, both = gu.shape
-        if both == 0 or both % 2:
-            raise ValueError("gu must have an even number of columns: gate, then up")
-        inner = both // 2
-        dev, wide = gu.device, fp8_cols(inner)
-        hq = _output(hq, "hq", torch.uint8, (tokens, wide), dev)
-        hs = _output(hs, "hs", torch.uint8, (tokens, fp8_scale_cols(inner)), dev)
-        if checkpoint:
-            cq = _output(cq, "cq", torch.uint8, (tokens, 2 * wide), dev)
-            cs = _output(cs, "cs", torch.uint8, (tokens, fp8_scale_cols(2 * wide)), dev)
-        elif cq is not None or cs is not None:
-            raise ValueError("cq and cs are outputs of checkpoint=True")
-        _check(_lib().taco_swiglu_quantize(gu.data_ptr(), tokens, inner, hq.data_ptr(), hs.data_ptr(), _ptr(cq),
-                                           _ptr(cs), _stream(dev, stream)))
-        return hq, hs, cq, cs
+    if stream is not None:
+        with _on(stream):
+            return swiglu_quantize(gu, checkpoint=checkpoint, hq=hq, hs=hs, cq=cq, cs=cs)
+    gu = _input(gu, "gu", torch.bfloat16)
+    tokens, both = gu.shape
+    if both == 0 or both % 2:
+        raise ValueError("gu must have an even number of columns: gate, then up")
+    inner = both // 2
+    dev, wide = gu.device, fp8_cols(inner)
+    hq = _output(hq, "hq", torch.uint8, (tokens, wide), dev)
+    hs = _output(hs, "hs", torch.uint8, (tokens, fp8_scale_cols(inner)), dev)
+    if checkpoint:
+        cq = _output(cq, "cq", torch.uint8, (tokens, 2 * wide), dev)
+        cs = _output(cs, "cs", torch.uint8, (tokens, fp8_scale_cols(2 * wide)), dev)
+    elif cq is not None or cs is not None:
+        raise ValueError("cq and cs are outputs of checkpoint=True")
+    _check(_lib().taco_swiglu_quantize(gu.data_ptr(), tokens, inner, hq.data_ptr(), hs.data_ptr(), _ptr(cq),
+                                       _ptr(cs), _current(dev)))
+    return hq, hs, cq, cs
 
 
 def swiglu_backward(dh: torch.Tensor, cq: torch.Tensor, cs: torch.Tensor, *, quantize: bool = True,
@@ -286,19 +303,21 @@ def swiglu_backward(dh: torch.Tensor, cq: torch.Tensor, cs: torch.Tensor, *, qua
 
     Returns (dgu bf16 [tokens, 2 * inner], dq, ds): the gradient of gu, and the
     same in the block format (quantize=False gives None for those)."""
-    with _on(stream):
-        dh = _input(dh, "dh", torch.bfloat16)
-        tokens, inner = dh.shape
-        wide = fp8_cols(inner)
-        cq = _input(cq, "cq", torch.uint8, (tokens, 2 * wide))
-        cs = _input(cs, "cs", torch.uint8, (tokens, fp8_scale_cols(2 * wide)))
-        dev = _same_device(dh, cq, cs)
-        dgu = _output(dgu, "dgu", torch.bfloat16, (tokens, 2 * inner), dev)
-        if quantize:
-            dq = _output(dq, "dq", torch.uint8, (tokens, fp8_cols(2 * inner)), dev)
-            ds = _output(ds, "ds", torch.uint8, (tokens, fp8_scale_cols(2 * inner)), dev)
-        elif dq is not None or ds is not None:
-            raise ValueError("dq and ds are outputs of quantize=True")
-        _check(_lib().taco_swiglu_backward(dh.data_ptr(), cq.data_ptr(), cs.data_ptr(), tokens, inner,
-                                           dgu.data_ptr(), _ptr(dq), _ptr(ds), _stream(dev, stream)))
-        return dgu, dq, ds
+    if stream is not None:
+        with _on(stream):
+            return swiglu_backward(dh, cq, cs, quantize=quantize, dgu=dgu, dq=dq, ds=ds)
+    dh = _input(dh, "dh", torch.bfloat16)
+    tokens, inner = dh.shape
+    wide = fp8_cols(inner)
+    dev = dh.device
+    cq = _shaped(cq, "cq", torch.uint8, (tokens, 2 * wide), dev)
+    cs = _shaped(cs, "cs", torch.uint8, (tokens, fp8_scale_cols(2 * wide)), dev)
+    dgu = _output(dgu, "dgu", torch.bfloat16, (tokens, 2 * inner), dev)
+    if quantize:
+        dq = _output(dq, "dq", torch.uint8, (tokens, fp8_cols(2 * inner)), dev)
+        ds = _output(ds, "ds", torch.uint8, (tokens, fp8_scale_cols(2 * inner)), dev)
+    elif dq is not None or ds is not None:
+        raise ValueError("dq and ds are outputs of quantize=True")
+    _check(_lib().taco_swiglu_backward(dh.data_ptr(), cq.data_ptr(), cs.data_ptr(), tokens, inner,
+                                       dgu.data_ptr(), _ptr(dq), _ptr(ds), _current(dev)))
+    return dgu, dq, ds

@@ -50,14 +50,32 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     pack_bf16x2(v[6], v[7]));
 }
 
+// The elements of v from e on, e in 0..7, moved to the front.
+__device__ __forceinline__ uint4 drop_elements(const uint4 v, int e) {
+  unsigned w[5] = {v.x, v.y, v.z, v.w, 0};
+  if (e & 4) w[0] = w[2], w[1] = w[3], w[2] = w[3] = 0;
+  if (e & 2) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = 0;
+  const unsigned bits = 16 * (e & 1);
+  return make_uint4(__builtin_amdgcn_alignbit(w[1], w[0], bits), __builtin_amdgcn_alignbit(w[2], w[1], bits),
+                    __builtin_amdgcn_alignbit(w[3], w[2], bits), __builtin_amdgcn_alignbit(w[4], w[3], bits));
+}
+
 // Elements [col, col + 8) of a bf16 row of `cols` elements; 0 past its end.
 // WIDE: cols is a multiple of 8 and the row 16-byte aligned, so a chunk lies
-// inside the row or outside it and moves in one piece.
+// inside the row or outside it.  Otherwise a row may start at any element (16
+// bytes are loaded at 2-byte alignment), and the chunk that crosses the row's
+// end is loaded from the last 8 elements and moved to the front.
 template <bool WIDE>
 __device__ __forceinline__ uint4 load_chunk(const uint16_t* row, int col, int cols) {
   uint4 u = make_uint4(0, 0, 0, 0);
   if constexpr (WIDE) {
     if (col < cols) u = *reinterpret_cast<const uint4*>(row + col);
+  } else if (cols >= 8) {
+    if (col < cols) {
+      const int from = min(col, cols - 8);
+      __builtin_memcpy(&u, row + from, 16);
+      u = drop_elements(u, col - from);
+    }
   } else {
     unsigned e[8];
 #pragma unroll
@@ -71,10 +89,12 @@ template <bool WIDE>
 __device__ __forceinline__ void store_chunk(uint16_t* row, int col, int cols, const uint4 u) {
   if constexpr (WIDE) {
     if (col < cols) *reinterpret_cast<uint4*>(row + col) = u;
+  } else if (col + 8 <= cols) {
+    __builtin_memcpy(row + col, &u, 16);
   } else {
     const unsigned w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 7; ++j)
       if (col + j < cols) row[col + j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
   }
 }

@@ -143,6 +143,23 @@ __device__ __forceinline__ void multiply(const i32x8_t (&b)[NT], const i32x8_t (
   __builtin_amdgcn_s_setprio(0);
 }
 
+// Four consecutive columns of an fp32 row.  The row may be of odd length: any
+// 4-byte alignment.
+__device__ __forceinline__ void store_sums(float* row, int col, int k, f32x4_t v, bool add) {
+  if (col + 4 <= k) {
+    if (add) {
+      f32x4_t o;
+      __builtin_memcpy(&o, row + col, 16);
+      v += o;
+    }
+    __builtin_memcpy(row + col, &v, 16);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 3; ++c)
+      if (col + c < k) row[col + c] = add ? row[col + c] + v[c] : v[c];
+  }
+}
+
 // Four consecutive columns of a row of y, from `col` on.  Rows of odd length
 // start at any element: the store is 8 bytes at 2-byte alignment.
 __device__ __forceinline__ void store_columns(uint16_t* out, int col, int n, const f32x4_t v) {
@@ -161,6 +178,9 @@ __device__ __forceinline__ void store_columns(uint16_t* out, int col, int n, con
 // which keeps a CU's memory pipeline busy where there are few tiles; their sums
 // are added in LDS at the end, in the groups' order.  Each group has a ring of
 // S steps in LDS, S - 1 of them on their way; one barrier per round of steps.
+// Where even so most CUs have no tile, k is also split over workgroups
+// (blockIdx.y, split_steps steps each): they write fp32 sums to `partial`, and
+// partial_sums_kernel adds those in order.
 template <int NT, int MT, int WN, int WM, int KG, int S>
 struct MatmulTile {
   static constexpr int kGroup = WN * WM, kThreads = 64 * kGroup * KG;
@@ -181,7 +201,8 @@ struct MatmulTile {
 template <int NT, int MT, int WN, int WM, int KG, int S>
 __global__ __launch_bounds__(64 * WN * WM * KG) void matmul_tiles_kernel(
     const uint8_t* __restrict__ qa, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ qb,
-    const uint8_t* __restrict__ sb, int m, int n, int kcols, int kscales, uint16_t* __restrict__ y) {
+    const uint8_t* __restrict__ sb, int m, int n, int kcols, int kscales, uint16_t* __restrict__ y, int split_steps,
+    float* __restrict__ partial) {
   using T = MatmulTile<NT, MT, WN, WM, KG, S>;
   __shared__ __align__(128) uint8_t lds[T::kLds];
   const int lane = threadIdx.x & 63;
@@ -231,13 +252,15 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void matmul_tiles_kernel(
 
   const int lane_off = r * kBlock + 16 * (g ^ (r & 7));
   f32x4_t acc[NT][MT] = {};
-  const int steps = kcols / kBlock;
-  if (group < steps) copy_scales(group);
+  // scale bytes come in dwords of four steps, so a split starts at a multiple of four
+  const int first = static_cast<int>(blockIdx.y) * split_steps;
+  const int steps = min(kcols / kBlock, first + split_steps);
+  if (first + group < steps) copy_scales(first + group);
 #pragma unroll
   for (int i = 0; i < S - 1; ++i)
-    if (group + i * KG < steps) copy_step(group + i * KG, i);
+    if (first + group + i * KG < steps) copy_step(first + group + i * KG, i);
   int slot = 0, round = 0;
-  for (int k = group; k < steps + group; k += KG, ++round) {
+  for (int k = first + group; k < steps + group; k += KG, ++round) {
     // step k has landed for all; what the step before it read has been multiplied
     if (k + (S - 2) * KG < steps)
       copies_left<(S - 2) * T::kCopies>();
@@ -282,6 +305,12 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void matmul_tiles_kernel(
   for (int j = 0; j < MT; ++j) {
     const int row = m0 + 16 * (MT * wm + j) + r;
     if (row >= m) continue;
+    if (partial != nullptr) {
+      float* out = partial + (static_cast<int64_t>(blockIdx.y) * m + row) * n;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) store_sums(out, n0 + 16 * (NT * wn + i) + 4 * g, n, acc[i][j], false);
+      continue;
+    }
     uint16_t* out = y + static_cast<int64_t>(row) * n;
 #pragma unroll
     for (int i = 0; i < NT; ++i) store_columns(out, n0 + 16 * (NT * wn + i) + 4 * g, n, acc[i][j]);
@@ -569,16 +598,6 @@ __device__ __forceinline__ bf16x8_t read_columns(const uint8_t* tile, int lane_o
 // it, in pieces of rows of any length from 8, or element by element.
 enum DyRows { kDyWhole, kDyOdd, kDyShort };
 
-// v >> 16 * e, e in 0..7: the elements from e on, first.
-__device__ __forceinline__ uint4 drop_elements(const uint4 v, int e) {
-  unsigned w[5] = {v.x, v.y, v.z, v.w, 0};
-  if (e & 4) w[0] = w[2], w[1] = w[3], w[2] = w[3] = 0;
-  if (e & 2) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = 0;
-  const unsigned bits = 16 * (e & 1);
-  return make_uint4(__builtin_amdgcn_alignbit(w[1], w[0], bits), __builtin_amdgcn_alignbit(w[2], w[1], bits),
-                    __builtin_amdgcn_alignbit(w[3], w[2], bits), __builtin_amdgcn_alignbit(w[4], w[3], bits));
-}
-
 // A step's part of dy that a thread moves: N pieces of 8 columns.  The loads
 // have no branch and nothing waits for them before store(): rows past the last
 // are read from the last and cleared on the way into LDS, pieces that cross the
@@ -682,22 +701,6 @@ __device__ __forceinline__ void multiply(const bf16x8_t (&x)[KT], const bf16x8_t
   __builtin_amdgcn_s_setprio(0);
 }
 
-// Four consecutive k of a row of dw.  k may be odd: any 4-byte alignment.
-__device__ __forceinline__ void store_gradient(float* row, int col, int k, f32x4_t v, bool add) {
-  if (col + 4 <= k) {
-    if (add) {
-      f32x4_t o;
-      __builtin_memcpy(&o, row + col, 16);
-      v += o;
-    }
-    __builtin_memcpy(row + col, &v, 16);
-  } else {
-#pragma unroll
-    for (int c = 0; c < 3; ++c)
-      if (col + c < k) row[col + c] = add ? row[col + c] + v[c] : v[c];
-  }
-}
-
 struct WgradArgs {
   const uint16_t* dy;
   const uint8_t *q, *scale;
@@ -758,7 +761,7 @@ __global__ __launch_bounds__(64 * WK * WN) void wgrad_tiles_kernel(const WgradAr
     if (row >= p.n) continue;
 #pragma unroll
     for (int i = 0; i < KT; ++i)
-      store_gradient(out + static_cast<int64_t>(row) * p.k, k0 + 16 * (KT * wk + i) + 4 * (lane >> 4), p.k, acc[i][j],
+      store_sums(out + static_cast<int64_t>(row) * p.k, k0 + 16 * (KT * wk + i) + 4 * (lane >> 4), p.k, acc[i][j],
                      p.add != 0);
   }
 }
@@ -898,38 +901,48 @@ __global__ __launch_bounds__(512) void wgrad_turns_kernel(const WgradArgs p) {
     if (row >= p.n) continue;
 #pragma unroll
     for (int i = 0; i < KT; ++i)
-      store_gradient(p.dw + static_cast<int64_t>(row) * p.k, k0 + 16 * (KT * wk + i) + 4 * (lane >> 4), p.k, acc[i][j],
+      store_sums(p.dw + static_cast<int64_t>(row) * p.k, k0 + 16 * (KT * wk + i) + 4 * (lane >> 4), p.k, acc[i][j],
                      p.add != 0);
   }
 }
 
-// dw = (dw +) the partial sums, in order.
-__global__ __launch_bounds__(256) void wgrad_sum_kernel(const float* __restrict__ partial, int64_t count, int splits,
-                                                        float* __restrict__ dw, int add) {
+// out = (out +) the partial sums, in order; fp32, or rounded once to bf16.
+template <typename T>
+__global__ __launch_bounds__(256) void partial_sums_kernel(const float* __restrict__ partial, int64_t count, int splits,
+                                                           T* __restrict__ out, int add) {
   const int64_t i = 4 * (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x);
   if (i >= count) return;
-  if (i + 4 <= count) {
-    f32x4_t v = {};
-    for (int s = 0; s < splits; ++s) {
+  const int here = static_cast<int>(min(count - i, int64_t(4)));
+  float v[4] = {};
+  for (int s = 0; s < splits; ++s) {
+    const float* p = partial + s * count + i;
+    if (here == 4) {
       f32x4_t o;
-      __builtin_memcpy(&o, partial + s * count + i, 16);
-      v += o;
-    }
-    if (add) v += *reinterpret_cast<const f32x4_t*>(dw + i);
-    *reinterpret_cast<f32x4_t*>(dw + i) = v;
-  } else {
-    for (int64_t j = i; j < count; ++j) {
-      float v = 0.0f;
-      for (int s = 0; s < splits; ++s) v += partial[s * count + j];
-      dw[j] = add ? v + dw[j] : v;
+      __builtin_memcpy(&o, p, 16);
+      for (int c = 0; c < 4; ++c) v[c] += o[c];
+    } else {
+      for (int c = 0; c < here; ++c) v[c] += p[c];
     }
   }
+  for (int c = 0; c < here; ++c) {
+    if constexpr (sizeof(T) == 2)
+      out[i + c] = static_cast<T>(pack_bf16x2(v[c], 0.0f));
+    else
+      out[i + c] = add ? v[c] + out[i + c] : v[c];
+  }
+}
+
+template <typename T>
+void launch_partial_sums(const float* partial, int64_t count, int splits, T* out, int add, hipStream_t stream) {
+  hipLaunchKernelGGL(partial_sums_kernel<T>, dim3(static_cast<unsigned>((count + 1023) / 1024)), dim3(256), 0, stream,
+                     partial, count, splits, out, add);
 }
 
 struct MatmulArgs {
   const uint8_t *qa, *sa, *qb, *sb;
   int m, n, kcols, kscales;
   uint16_t* y;
+  float* workspace;
 };
 
 int64_t tiles_of(int64_t m, int64_t n, int64_t bm, int64_t bn) { return (m + bm - 1) / bm * ((n + bn - 1) / bn); }
@@ -940,12 +953,33 @@ void launch_few(const MatmulArgs& p, hipStream_t stream) {
                      p.sb, p.m, p.n, p.kcols, p.kscales, p.y);
 }
 
+// splits workgroups to a tile, of split_steps steps (a multiple of four) each.
 template <int NT, int MT, int WN, int WM, int KG, int S>
-void launch_tiles(const MatmulArgs& p, hipStream_t stream) {
+void launch_tiles(const MatmulArgs& p, hipStream_t stream, int splits = 1, int split_steps = 1 << 30) {
   using T = MatmulTile<NT, MT, WN, WM, KG, S>;
   hipLaunchKernelGGL((matmul_tiles_kernel<NT, MT, WN, WM, KG, S>),
-                     dim3(static_cast<unsigned>(tiles_of(p.m, p.n, T::BM, T::BN))), dim3(T::kThreads), 0, stream, p.qa,
-                     p.sa, p.qb, p.sb, p.m, p.n, p.kcols, p.kscales, p.y);
+                     dim3(static_cast<unsigned>(tiles_of(p.m, p.n, T::BM, T::BN)), splits), dim3(T::kThreads), 0,
+                     stream, p.qa, p.sa, p.qb, p.sb, p.m, p.n, p.kcols, p.kscales, p.y, split_steps,
+                     splits > 1 ? p.workspace : nullptr);
+}
+
+// Workgroups to a tile of 64 x 64, and their steps: at least about sixteen, and
+// no more workgroups than CUs.  Measured (us, with the sums' kernel):
+//   m     n     k      one   two   four
+//   300   512   8192   18.7  -     12.1
+//   1000  200   8192   18.8  13.7  11.6
+//   100   1601  4096   11.3  10.4  9.9
+//   64    4096  4096   10.8  10.6  10.8
+//   200   1024  2048   7.1   8.9   -
+struct Splits {
+  int count, steps;
+};
+Splits matmul_splits(int64_t m, int64_t n, int64_t kcols) {
+  const int64_t steps = kcols / kBlock, tiles = tiles_of(m, n, 64, 64);
+  const int64_t most = std::min(256 / tiles, steps / 16);
+  if (m <= 32 || most < 2) return {1, 1 << 30};
+  const int64_t each = (steps + 4 * most - 1) / (4 * most) * 4;
+  return {static_cast<int>((steps + each - 1) / each), static_cast<int>(each)};
 }
 
 void launch_big(const MatmulArgs& p, hipStream_t stream) {
@@ -974,7 +1008,10 @@ void launch_matmul(const MatmulArgs& p, hipStream_t stream) {
     launch_few<1>(p, stream);
   else if (p.m <= 32)
     launch_few<2>(p, stream);
-  else if (t64 <= 256)
+  else if (const Splits s = matmul_splits(p.m, p.n, p.kcols); s.count > 1) {
+    launch_tiles<2, 2, 2, 2, 2, 4>(p, stream, s.count, s.steps);
+    launch_partial_sums(p.workspace, static_cast<int64_t>(p.m) * p.n, s.count, p.y, 0, stream);
+  } else if (t64 <= 256)
     launch_tiles<2, 2, 2, 2, 2, 4>(p, stream);
   else if (t64 <= 768)
     launch_tiles<2, 2, 2, 2, 1, 3>(p, stream);
@@ -1031,9 +1068,7 @@ void launch_wgrad(const WgradArgs& args, float* workspace, hipStream_t stream) {
     p.dw = workspace;
     p.add = 0;
     launch_wgrad_tiles<2, 2, 2, 2>(p, stream);
-    const int64_t count = static_cast<int64_t>(p.n) * p.k;
-    hipLaunchKernelGGL(wgrad_sum_kernel, dim3(static_cast<unsigned>((count + 1023) / 1024)), dim3(256), 0, stream,
-                       workspace, count, p.splits, args.dw, args.add);
+    launch_partial_sums(workspace, static_cast<int64_t>(p.n) * p.k, p.splits, args.dw, args.add, stream);
   } else if (tiles_of(p.n, p.k, 64, 64) <= 1024) {
     launch_wgrad_tiles<2, 2, 2, 2>(p, stream);
   } else if (tiles_of(p.n, p.k, 256, 256) < 192) {
@@ -1047,7 +1082,11 @@ void launch_wgrad(const WgradArgs& args, float* workspace, hipStream_t stream) {
 
 extern "C" {
 
-size_t taco_matmul_fp8_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t taco_matmul_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (!matrix_ok(m, k) || !matrix_ok(n, k) || m > kMaxCodes / n) return 0;
+  const int splits = matmul_splits(m, n, fp8_cols(k)).count;
+  return splits > 1 ? static_cast<size_t>(4 * m * n) * splits : 0;
+}
 
 taco_status_t taco_matmul_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb, int64_t m,
                               int64_t n, int64_t k, void* y_bf16, void* workspace, size_t workspace_bytes,
@@ -1057,14 +1096,16 @@ taco_status_t taco_matmul_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_
   if (!aligned(qa, 16) || !aligned(qb, 16) || !aligned(y_bf16, 16) || !aligned(sa, 4) || !aligned(sb, 4) ||
       !aligned(workspace, 256))
     return TACO_ERR_ALIGN;
-  if (workspace_bytes < taco_matmul_fp8_workspace_bytes(m, n, k)) return TACO_ERR_WORKSPACE;
+  if (const size_t need = taco_matmul_fp8_workspace_bytes(m, n, k);
+      need > 0 && (!workspace || workspace_bytes < need))
+    return TACO_ERR_WORKSPACE;
   const int64_t kcols = fp8_cols(k), kscales = fp8_scale_cols(k);
   if (aliased({{y_bf16, static_cast<size_t>(2 * m * n)}, {workspace, workspace_bytes}},
               {{qa, static_cast<size_t>(m * kcols)}, {sa, static_cast<size_t>(m * kscales)},
                {qb, static_cast<size_t>(n * kcols)}, {sb, static_cast<size_t>((n + kBlock - 1) / kBlock * kscales)}}))
     return TACO_ERR_ALIAS;
   launch_matmul({qa, sa, qb, sb, static_cast<int>(m), static_cast<int>(n), static_cast<int>(kcols),
-                 static_cast<int>(kscales), static_cast<uint16_t*>(y_bf16)}, stream);
+                 static_cast<int>(kscales), static_cast<uint16_t*>(y_bf16), static_cast<float*>(workspace)}, stream);
   return launched();
 }
 
@@ -1082,7 +1123,9 @@ taco_status_t taco_wgrad_fp8(const void* dy_bf16, const uint8_t* q, const uint8_
     return TACO_ERR_SHAPE;
   if (!aligned(dy_bf16, 16) || !aligned(q, 16) || !aligned(dw, 16) || !aligned(scale, 4) || !aligned(workspace, 256))
     return TACO_ERR_ALIGN;
-  if (workspace_bytes < taco_wgrad_fp8_workspace_bytes(tokens, n, k)) return TACO_ERR_WORKSPACE;
+  if (const size_t need = taco_wgrad_fp8_workspace_bytes(tokens, n, k);
+      need > 0 && (!workspace || workspace_bytes < need))
+    return TACO_ERR_WORKSPACE;
   const int64_t kcols = fp8_cols(k), kscales = fp8_scale_cols(k);
   if (aliased({{dw, static_cast<size_t>(4 * n * k)}, {workspace, workspace_bytes}},
               {{dy_bf16, static_cast<size_t>(2 * tokens * n)}, {q, static_cast<size_t>(tokens * kcols)},

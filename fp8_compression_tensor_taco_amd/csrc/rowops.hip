@@ -205,110 +205,150 @@ __global__ __launch_bounds__(RowGroup<WPR>::kWG) void rmsnorm_quantize_kernel(
   pad_scales(sr, chunks / kBlockChunks, static_cast<int>(scols), thread);
 }
 
-// The gradient.  Each wavefront (or WPR of them) walks rows gridDim.x * kRows
-// apart and keeps its columns' sums of dy * xhat in registers; a workgroup
-// writes them once, as one row of `partial`, and column_sums_kernel adds the
-// workgroups' rows in order.
-constexpr int kBackwardWaves = 8;                   // rows of a workgroup where a row is one wavefront's
-
-template <int WPR>
-struct BackwardGroup {
-  static constexpr int kRows = WPR == 1 ? kBackwardWaves : 1;
-  static constexpr int kWG = 64 * kRows * WPR;
-};
-
-template <int WPR, int CH, bool WIDE>
-__global__ __launch_bounds__(BackwardGroup<WPR>::kWG) void rmsnorm_backward_kernel(
+// The gradient.  A workgroup of WAVES wavefronts holds R whole rows at a time
+// (CH chunks per lane and row), walks the rows gridDim.x * R apart and keeps its
+// columns' sums of dy * xhat in registers; it writes them once, as one row of
+// `partial`, and column_sums_kernel adds the workgroups' rows in order.  Two
+// rows at a time and two or more workgroups per CU keep the loads going across
+// the rows' reductions.
+template <int WAVES, int CH, int R, bool WIDE>
+__global__ __launch_bounds__(64 * WAVES) void rmsnorm_backward_kernel(
     const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, const float* __restrict__ rstd,
     const uint16_t* __restrict__ weight, const uint16_t* __restrict__ dz, int64_t rows, int cols,
     uint16_t* __restrict__ dx, float* __restrict__ partial) {
-  constexpr int kRows = BackwardGroup<WPR>::kRows;
-  __shared__ float red[2][WPR];                     // two sets: one barrier per row is enough
-  __shared__ __align__(16) float sums[WPR == 1 ? 512 * CH : 4];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int first = (WPR == 1 ? 0 : 64 * wave) + lane;
+  __shared__ float red[2][R][WAVES];                // two sets: one barrier per turn is enough
+  const int wave = threadIdx.x >> 6;
   const float inv_cols = 1.0f / static_cast<float>(cols);
+  auto column = [&](int i) { return 8 * static_cast<int>(threadIdx.x + 64 * WAVES * i); };
   uint4 w[CH];
   float acc[CH][8];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    w[i] = load_chunk<WIDE>(weight, 8 * (first + 64 * WPR * i), cols);
+    w[i] = load_chunk<WIDE>(weight, column(i), cols);
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
   }
   int parity = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (WPR == 1 ? wave : 0); row < rows;
-       row += static_cast<int64_t>(gridDim.x) * kRows, parity ^= 1) {
-    uint4 g[CH], x[CH], add[CH];
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * R; row0 < rows;
+       row0 += static_cast<int64_t>(gridDim.x) * R, parity ^= 1) {
+    uint4 g[R][CH], x[R][CH], add[R][CH];
+    float r[R], c[R];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      g[i] = load_chunk<WIDE>(dy + row * cols, 8 * (first + 64 * WPR * i), cols);
-      x[i] = load_chunk<WIDE>(z + row * cols, 8 * (first + 64 * WPR * i), cols);
-      if (dz != nullptr) add[i] = load_chunk<WIDE>(dz + row * cols, 8 * (first + 64 * WPR * i), cols);
-    }
-    const float r = rstd[row];
-    float c = 0.0f;
+    for (int k = 0; k < R; ++k) {
+      const int64_t row = min(row0 + k, rows - 1);
+      r[k] = rstd[row];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      float a[8], b[8], ww[8];
-      unpack8(g[i], a);
-      unpack8(x[i], b);
-      unpack8(w[i], ww);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float xhat = b[j] * r;
-        acc[i][j] = fmaf(a[j], xhat, acc[i][j]);
-        c = fmaf(a[j] * ww[j], xhat, c);
+      for (int i = 0; i < CH; ++i) {
+        g[k][i] = load_chunk<WIDE>(dy + row * cols, column(i), cols);
+        x[k][i] = load_chunk<WIDE>(z + row * cols, column(i), cols);
+        if (dz != nullptr) add[k][i] = load_chunk<WIDE>(dz + row * cols, column(i), cols);
       }
     }
-    c = row_sum<WPR>(c, red[parity]) * inv_cols;
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      float a[8], b[8], ww[8];
-      unpack8(g[i], a);
-      unpack8(x[i], b);
-      unpack8(w[i], ww);
+    for (int k = 0; k < R; ++k) {
+      c[k] = 0.0f;
+      if (row0 + k < rows) {                        // the whole workgroup alike
 #pragma unroll
-      for (int j = 0; j < 8; ++j) a[j] = r * (a[j] * ww[j] - b[j] * r * c);
-      if (dz != nullptr) {
-        unpack8(add[i], b);
+        for (int i = 0; i < CH; ++i) {
+          float a[8], b[8], ww[8];
+          unpack8(g[k][i], a);
+          unpack8(x[k][i], b);
+          unpack8(w[i], ww);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] += b[j];
+          for (int j = 0; j < 8; ++j) {
+            const float xhat = b[j] * r[k];
+            acc[i][j] = fmaf(a[j], xhat, acc[i][j]);
+            c[k] = fmaf(a[j] * ww[j], xhat, c[k]);
+          }
+        }
       }
-      store_chunk<WIDE>(dx + row * cols, 8 * (first + 64 * WPR * i), cols, pack8(a));
+      c[k] = wave_sum(c[k]);
+      if ((threadIdx.x & 63) == 0) red[parity][k][wave] = c[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (row0 + k >= rows) continue;
+      float sum = red[parity][k][0];
+#pragma unroll
+      for (int v = 1; v < WAVES; ++v) sum += red[parity][k][v];
+      sum *= inv_cols;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        float a[8], b[8], ww[8];
+        unpack8(g[k][i], a);
+        unpack8(x[k][i], b);
+        unpack8(w[i], ww);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = r[k] * (a[j] * ww[j] - b[j] * r[k] * sum);
+        if (dz != nullptr) {
+          unpack8(add[k][i], b);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) a[j] += b[j];
+        }
+        store_chunk<WIDE>(dx + (row0 + k) * cols, column(i), cols, pack8(a));
+      }
     }
   }
   const int64_t stride = fp8_cols(cols);
   float* out = partial + static_cast<int64_t>(blockIdx.x) * stride;
-  if constexpr (WPR == 1) {
-    for (int v = 0; v < kRows; ++v) {               // the wavefronts add in turn
-      if (wave == v) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; j += 4) {
-            float4* p = reinterpret_cast<float4*>(&sums[8 * (lane + 64 * i) + j]);
-            float4 s = make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
-            if (v != 0) {
-              const float4 o = *p;
-              s = make_float4(s.x + o.x, s.y + o.y, s.z + o.z, s.w + o.w);
-            }
-            *p = s;
-          }
-      }
-      __syncthreads();
+  for (int i = 0; i < CH; ++i)
+    if (column(i) < stride) {
+      *reinterpret_cast<float4*>(out + column(i)) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      *reinterpret_cast<float4*>(out + column(i) + 4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
     }
-    for (int c = 4 * threadIdx.x; c < stride; c += 4 * BackwardGroup<WPR>::kWG)
-      *reinterpret_cast<float4*>(out + c) = *reinterpret_cast<const float4*>(&sums[c]);
-  } else {
+}
+
+// Rows too long for that: first mean(dy * weight * xhat) of each row, a
+// workgroup per row, then the rest by pieces of 2048 columns.
+template <bool WIDE>
+__global__ __launch_bounds__(kThreads) void rmsnorm_row_means_kernel(
+    const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, const float* __restrict__ rstd,
+    const uint16_t* __restrict__ weight, int cols, float* __restrict__ means) {
+  __shared__ float red[kWaves];
+  const int64_t row = blockIdx.x;
+  const float r = rstd[row];
+  float c = 0.0f;
+  for (int col = 8 * threadIdx.x; col < cols; col += 8 * kThreads) {
+    float a[8], b[8], ww[8];
+    unpack8(load_chunk<WIDE>(dy + row * cols, col, cols), a);
+    unpack8(load_chunk<WIDE>(z + row * cols, col, cols), b);
+    unpack8(load_chunk<WIDE>(weight, col, cols), ww);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = 8 * (first + 64 * WPR * i);
-      if (c < stride) {
-        *reinterpret_cast<float4*>(out + c) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-        *reinterpret_cast<float4*>(out + c + 4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
-      }
+    for (int j = 0; j < 8; ++j) c = fmaf(a[j] * ww[j], b[j] * r, c);
+  }
+  c = row_sum<kWaves>(c, red);
+  if (threadIdx.x == 0) means[row] = c / static_cast<float>(cols);
+}
+
+template <bool WIDE>
+__global__ __launch_bounds__(kThreads) void rmsnorm_backward_long_kernel(
+    const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, const float* __restrict__ rstd,
+    const uint16_t* __restrict__ weight, const uint16_t* __restrict__ dz, int64_t rows, int cols,
+    const float* __restrict__ means, uint16_t* __restrict__ dx, float* __restrict__ partial) {
+  const int col = 8 * (kThreads * blockIdx.y + threadIdx.x);
+  float ww[8], acc[8] = {};
+  unpack8(load_chunk<WIDE>(weight, col, cols), ww);
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const float r = rstd[row], c = means[row];
+    float a[8], b[8], v[8] = {};
+    unpack8(load_chunk<WIDE>(dy + row * cols, col, cols), a);
+    unpack8(load_chunk<WIDE>(z + row * cols, col, cols), b);
+    if (dz != nullptr) unpack8(load_chunk<WIDE>(dz + row * cols, col, cols), v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float xhat = b[j] * r;
+      acc[j] = fmaf(a[j], xhat, acc[j]);
+      v[j] += r * (a[j] * ww[j] - xhat * c);
     }
+    store_chunk<WIDE>(dx + row * cols, col, cols, pack8(v));
+  }
+  const int64_t stride = fp8_cols(cols);
+  if (col < stride) {
+    float* out = partial + static_cast<int64_t>(blockIdx.x) * stride + col;
+    *reinterpret_cast<float4*>(out) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    *reinterpret_cast<float4*>(out + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
   }
 }
 
@@ -490,24 +530,44 @@ void launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t*
                        eps, z, rstd, q, scale);
 }
 
-// Workgroups of the norm's gradient: one per 8 rows (or row), at most kMaxGroups.
-constexpr int64_t kMaxGroups = 256;
+// Workgroups of the norm's gradient, each with a row of partial sums.
+constexpr int64_t kMaxGroups = 512;
+constexpr int64_t kLongRow = 16384;                 // columns that a workgroup holds at most
+constexpr int rows_at_a_time(int64_t cols) { return cols <= 8192 ? 2 : 1; }
 int backward_groups(int64_t rows, int64_t cols) {
-  const int64_t per = cols <= 4096 ? kBackwardWaves : 1;
-  return static_cast<int>(std::min<int64_t>((rows + per - 1) / per, kMaxGroups));
+  const int64_t most = cols > kLongRow ? 64 : kMaxGroups;       // of long rows there are several pieces besides
+  return static_cast<int>(std::min<int64_t>((rows + rows_at_a_time(cols) - 1) / rows_at_a_time(cols), most));
 }
 
-template <int WPR, int CH>
-void launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* z, const float* rstd, const uint16_t* weight,
-                             const uint16_t* dz, int64_t rows, int cols, uint16_t* dx, float* partial,
-                             hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(backward_groups(rows, cols))), wg(BackwardGroup<WPR>::kWG);
-  if (cols % 8 == 0)
-    hipLaunchKernelGGL((rmsnorm_backward_kernel<WPR, CH, true>), grid, wg, 0, stream, dy, z, rstd, weight, dz, rows,
-                       cols, dx, partial);
+struct NormGradient {
+  const uint16_t *dy, *z;
+  const float* rstd;
+  const uint16_t *weight, *dz;
+  int64_t rows;
+  int cols;
+  uint16_t* dx;
+  float *partial, *means;
+};
+
+template <int WAVES, int CH>
+void launch_rmsnorm_backward(const NormGradient& p, hipStream_t stream) {
+  constexpr int R = rows_at_a_time(512 * WAVES * CH);
+  const dim3 grid(static_cast<unsigned>(backward_groups(p.rows, p.cols))), wg(64 * WAVES);
+  if (p.cols % 8 == 0)
+    hipLaunchKernelGGL((rmsnorm_backward_kernel<WAVES, CH, R, true>), grid, wg, 0, stream, p.dy, p.z, p.rstd,
+                       p.weight, p.dz, p.rows, p.cols, p.dx, p.partial);
   else
-    hipLaunchKernelGGL((rmsnorm_backward_kernel<WPR, CH, false>), grid, wg, 0, stream, dy, z, rstd, weight, dz, rows,
-                       cols, dx, partial);
+    hipLaunchKernelGGL((rmsnorm_backward_kernel<WAVES, CH, R, false>), grid, wg, 0, stream, p.dy, p.z, p.rstd,
+                       p.weight, p.dz, p.rows, p.cols, p.dx, p.partial);
+}
+
+template <bool WIDE>
+void launch_rmsnorm_backward_long(const NormGradient& p, hipStream_t stream) {
+  hipLaunchKernelGGL(rmsnorm_row_means_kernel<WIDE>, dim3(static_cast<unsigned>(p.rows)), dim3(kThreads), 0, stream,
+                     p.dy, p.z, p.rstd, p.weight, p.cols, p.means);
+  const dim3 grid(static_cast<unsigned>(backward_groups(p.rows, p.cols)), (p.cols + 8 * kThreads - 1) / (8 * kThreads));
+  hipLaunchKernelGGL(rmsnorm_backward_long_kernel<WIDE>, grid, dim3(kThreads), 0, stream, p.dy, p.z, p.rstd, p.weight,
+                     p.dz, p.rows, p.cols, p.means, p.dx, p.partial);
 }
 
 constexpr int64_t kMaxNormCols = 65536;
@@ -587,7 +647,7 @@ taco_status_t taco_rmsnorm_quantize(const void* x, const void* residual, const v
 
 size_t taco_rmsnorm_backward_workspace_bytes(int64_t tokens, int64_t hidden) {
   if (!matrix_ok(tokens, hidden) || hidden > kMaxNormCols) return 0;
-  return bytes(backward_groups(tokens, hidden), fp8_cols(hidden), 4);
+  return bytes(backward_groups(tokens, hidden), fp8_cols(hidden), 4) + (hidden > kLongRow ? bytes(tokens, 4) : 0);
 }
 
 taco_status_t taco_rmsnorm_backward(const void* dy, const void* z, const float* rstd, const void* weight,
@@ -603,13 +663,26 @@ taco_status_t taco_rmsnorm_backward(const void* dy, const void* z, const float* 
   if (aliased({{dx, n}, {dweight, bytes(hidden, 4)}, {workspace, workspace_bytes}},
               {{dy, n}, {z, n}, {rstd, bytes(tokens, 4)}, {weight, bytes(hidden, 2)}, {dz, n}}))
     return TACO_ERR_ALIAS;
-  const auto launch = hidden <= 2048 ? launch_rmsnorm_backward<1, 4> : hidden <= 4096 ? launch_rmsnorm_backward<1, 8>
-                    : hidden <= 16384 ? launch_rmsnorm_backward<4, 8> : launch_rmsnorm_backward<16, 8>;
-  launch(static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(z), rstd, static_cast<const uint16_t*>(weight),
-         static_cast<const uint16_t*>(dz), tokens, static_cast<int>(hidden), static_cast<uint16_t*>(dx),
-         static_cast<float*>(workspace), stream);
+  auto* partial = static_cast<float*>(workspace);
+  const int groups = backward_groups(tokens, hidden);
+  const NormGradient p{static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(z), rstd,
+                       static_cast<const uint16_t*>(weight), static_cast<const uint16_t*>(dz), tokens,
+                       static_cast<int>(hidden), static_cast<uint16_t*>(dx), partial,
+                       partial + groups * fp8_cols(hidden)};
+  if (hidden <= 2048)
+    launch_rmsnorm_backward<4, 1>(p, stream);
+  else if (hidden <= 4096)
+    launch_rmsnorm_backward<4, 2>(p, stream);
+  else if (hidden <= 8192)
+    launch_rmsnorm_backward<8, 2>(p, stream);
+  else if (hidden <= kLongRow)
+    launch_rmsnorm_backward<16, 2>(p, stream);
+  else if (hidden % 8 == 0)
+    launch_rmsnorm_backward_long<true>(p, stream);
+  else
+    launch_rmsnorm_backward_long<false>(p, stream);
   hipLaunchKernelGGL(column_sums_kernel, dim3(static_cast<unsigned>((hidden + 63) / 64)), dim3(64 * kSumClasses), 0,
-                     stream, static_cast<const float*>(workspace), backward_groups(tokens, hidden),
+                     stream, partial, groups,
                      static_cast<int>(hidden), fp8_cols(hidden), dweight);
   return launched();
 }
