@@ -352,23 +352,35 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_backward_long_kernel(
   }
 }
 
-// out[c] = the sum of partial[0..groups)[c], 64 columns and 16 row classes per workgroup.
-constexpr int kSumClasses = 16;
-__global__ __launch_bounds__(64 * kSumClasses) void column_sums_kernel(const float* __restrict__ partial, int groups,
-                                                                       int cols, int64_t stride,
-                                                                       float* __restrict__ out) {
-  __shared__ float red[kSumClasses][64];
-  const int lane = threadIdx.x & 63, cls = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
-  float s = 0.0f;
-  if (c < cols)
-    for (int g = cls; g < groups; g += kSumClasses) s += partial[g * stride + c];
-  red[cls][lane] = s;
-  __syncthreads();
-  if (cls == 0 && c < cols) {
+// out[c] = the sum of partial[0..groups)[c]: 16 columns per workgroup, four per
+// lane, 256 row classes.  Many workgroups and few rows each: the sums are in the
+// last-level cache and the reads' latency is the time.
+constexpr int kSumClasses = 256;
+__global__ __launch_bounds__(4 * kSumClasses) void column_sums_kernel(const float* __restrict__ partial, int groups,
+                                                                      int cols, int64_t stride,
+                                                                      float* __restrict__ out) {
+  __shared__ float4 red[kSumClasses][4];
+  const int part = threadIdx.x & 3, cls = threadIdx.x >> 2;
+  const int c = blockIdx.x * 16 + 4 * part;         // inside the padded row
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int g = cls; g < groups; g += kSumClasses) {
+    const float4 v = *reinterpret_cast<const float4*>(partial + g * stride + c);
+    s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+  }
+  red[cls][part] = s;
+  for (int half = kSumClasses / 2; half > 0; half >>= 1) {
+    __syncthreads();
+    if (cls < half) {
+      const float4 v = red[cls + half][part];
+      s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+      red[cls][part] = s;
+    }
+  }
+  if (cls == 0) {
+    const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-    for (int k = 1; k < kSumClasses; ++k) s += red[k][lane];
-    out[c] = s;
+    for (int j = 0; j < 4; ++j)
+      if (c + j < cols) out[c + j] = v[j];
   }
 }
 
@@ -475,7 +487,9 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
 }
 
 // Any other inner: a block of dgu's columns may hold the end of dg and the
-// start of du, so a lane computes the 8 output columns it holds one by one.
+// start of du, so a lane computes the 8 output columns it holds: all of dg or
+// all of du, from 8 columns of dh and of the checkpoint at any alignment and in
+// at most two blocks, or, where the two meet and at the end, one by one.
 __global__ __launch_bounds__(kThreads) void swiglu_backward_any_kernel(
     const uint16_t* __restrict__ dh, const uint8_t* __restrict__ cq, const uint8_t* __restrict__ cs, int64_t rows,
     int inner, int segments, uint16_t* __restrict__ dgu, uint8_t* __restrict__ dq, uint8_t* __restrict__ ds) {
@@ -487,22 +501,45 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_any_kernel(
   const int64_t dcols = fp8_cols(2 * static_cast<int64_t>(inner)), dscols = fp8_scale_cols(2 * static_cast<int64_t>(inner));
   const int blocks = static_cast<int>(pcols / kBlock), chunks = static_cast<int>(dcols / 8);
   const uint8_t *cr = cq + row * 2 * pcols, *csr = cs + row * ccols;
-  const int chunk = 64 * seg + lane;
-  float v[8];
+  const uint16_t* dr = dh + row * inner;
+  const int chunk = 64 * seg + lane, c0 = 8 * chunk;
+  const bool up = c0 >= inner;                      // of the chunk's first column
+  const int i0 = up ? c0 - inner : c0;
+  float v[8] = {};
+  if (i0 + 8 <= inner) {
+    uint4 d;
+    uint2 gq, uq;
+    __builtin_memcpy(&d, dr + i0, 16);
+    __builtin_memcpy(&gq, cr + i0, 8);
+    __builtin_memcpy(&uq, cr + pcols + i0, 8);
+    const int b0 = i0 / kBlock, b1 = (i0 + 7) / kBlock, split = b1 * kBlock - i0;     // columns from split on are in b1
+    const float gs0 = scale_value(csr[b0]), gs1 = scale_value(csr[b1]);
+    const float us0 = scale_value(csr[blocks + b0]), us1 = scale_value(csr[blocks + b1]);
+    float dv[8], g[8], u[8];
+    unpack8(d, dv);
+    decode8(gq, 1.0f, g);
+    decode8(uq, 1.0f, u);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int c = 8 * chunk + j;
-    v[j] = 0.0f;
-    if (c < 2 * inner) {
-      const int i = c < inner ? c : c - inner;
-      const float g = __builtin_amdgcn_cvt_f32_fp8(cr[i], 0) * scale_value(csr[i / kBlock]);
-      const float u = __builtin_amdgcn_cvt_f32_fp8(cr[pcols + i], 0) * scale_value(csr[blocks + i / kBlock]);
+    for (int j = 0; j < 8; ++j) {
       float dg, du;
-      swiglu_gradient(bf16_lo(dh[row * inner + i]), g, u, dg, du);
-      v[j] = c < inner ? dg : du;
+      swiglu_gradient(dv[j], g[j] * (j < split ? gs0 : gs1), u[j] * (j < split ? us0 : us1), dg, du);
+      v[j] = up ? du : dg;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = c0 + j;
+      if (c < 2 * inner) {
+        const int i = c < inner ? c : c - inner;
+        const float g = __builtin_amdgcn_cvt_f32_fp8(cr[i], 0) * scale_value(csr[i / kBlock]);
+        const float u = __builtin_amdgcn_cvt_f32_fp8(cr[pcols + i], 0) * scale_value(csr[blocks + i / kBlock]);
+        float dg, du;
+        swiglu_gradient(bf16_lo(dr[i]), g, u, dg, du);
+        v[j] = c < inner ? dg : du;
+      }
     }
   }
-  store_chunk<false>(dgu + row * 2 * inner, 8 * chunk, 2 * inner, pack8(v));
+  store_chunk<false>(dgu + row * 2 * inner, c0, 2 * inner, pack8(v));
   if (dq != nullptr) {
     quantize_chunk(v, dq + row * dcols, ds + row * dscols, chunk, chunks);
     if (seg == segments - 1) pad_scales(ds + row * dscols, chunks / kBlockChunks, static_cast<int>(dscols), lane);
@@ -531,11 +568,11 @@ void launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t*
 }
 
 // Workgroups of the norm's gradient, each with a row of partial sums.
-constexpr int64_t kMaxGroups = 512;
+constexpr int64_t kMaxGroups = 512;                 // of four wavefronts, more of fewer
 constexpr int64_t kLongRow = 16384;                 // columns that a workgroup holds at most
 constexpr int rows_at_a_time(int64_t cols) { return cols <= 8192 ? 2 : 1; }
 int backward_groups(int64_t rows, int64_t cols) {
-  const int64_t most = cols > kLongRow ? 64 : kMaxGroups;       // of long rows there are several pieces besides
+  const int64_t most = cols > kLongRow ? 64 : cols > 1024 ? kMaxGroups : cols > 512 ? 2 * kMaxGroups : 4 * kMaxGroups;
   return static_cast<int>(std::min<int64_t>((rows + rows_at_a_time(cols) - 1) / rows_at_a_time(cols), most));
 }
 
@@ -669,7 +706,11 @@ taco_status_t taco_rmsnorm_backward(const void* dy, const void* z, const float* 
                        static_cast<const uint16_t*>(weight), static_cast<const uint16_t*>(dz), tokens,
                        static_cast<int>(hidden), static_cast<uint16_t*>(dx), partial,
                        partial + groups * fp8_cols(hidden)};
-  if (hidden <= 2048)
+  if (hidden <= 512)
+    launch_rmsnorm_backward<1, 1>(p, stream);
+  else if (hidden <= 1024)
+    launch_rmsnorm_backward<2, 1>(p, stream);
+  else if (hidden <= 2048)
     launch_rmsnorm_backward<4, 1>(p, stream);
   else if (hidden <= 4096)
     launch_rmsnorm_backward<4, 2>(p, stream);
@@ -681,7 +722,7 @@ taco_status_t taco_rmsnorm_backward(const void* dy, const void* z, const float* 
     launch_rmsnorm_backward_long<true>(p, stream);
   else
     launch_rmsnorm_backward_long<false>(p, stream);
-  hipLaunchKernelGGL(column_sums_kernel, dim3(static_cast<unsigned>((hidden + 63) / 64)), dim3(64 * kSumClasses), 0,
+  hipLaunchKernelGGL(column_sums_kernel, dim3(static_cast<unsigned>((hidden + 15) / 16)), dim3(4 * kSumClasses), 0,
                      stream, partial, groups,
                      static_cast<int>(hidden), fp8_cols(hidden), dweight);
   return launched();
