@@ -539,13 +539,23 @@ __global__ __launch_bounds__(512) void matmul_turns_kernel(
     run(std::true_type{});
   else
     run(std::false_type{});
+  // A wavefront's 64 x 128 results go through LDS, so that a store covers four
+  // whole rows of 256 bytes and not 16 pieces of 32.
+  constexpr int kRow = 256 + 16;                   // bytes, apart by a bank group
+  __syncthreads();
+  uint8_t* mine = lds + wave * (64 * kRow);
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int row = m0 + 16 * (MT * wm + j) + r;
-    if (row >= m) continue;
-    uint16_t* out = y + static_cast<int64_t>(row) * n;
+  for (int j = 0; j < MT; ++j)
 #pragma unroll
-    for (int i = 0; i < NT; ++i) store_columns(out, n0 + 16 * (NT * wn + i) + 4 * g, n, acc[i][j]);
+    for (int i = 0; i < NT; ++i)
+      *reinterpret_cast<uint2*>(mine + (16 * j + r) * kRow + 2 * (16 * i + 4 * g)) =
+          make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
+  const int col = n0 + 128 * wn + 8 * r;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int row = m0 + 64 * wm + 4 * i + g;
+    const uint4 v = *reinterpret_cast<const uint4*>(mine + (4 * i + g) * kRow + 16 * r);
+    if (row < m) store_chunk<false>(y + static_cast<int64_t>(row) * n, col, n, v);
   }
 }
 
@@ -895,14 +905,25 @@ __global__ __launch_bounds__(512) void wgrad_turns_kernel(const WgradArgs p) {
       multiply(fx, fd, acc, [](int) {});
     }
   }
+  // Sixteen rows of 128 results at a time go through LDS, so that a store covers
+  // two whole rows of 512 bytes and not 16 pieces of 64.
+  constexpr int kRow = 512 + 16;                   // bytes, apart by a bank group
+  __syncthreads();
+  uint8_t* mine = lds + wave * (16 * kRow);
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int row = n0 + 16 * (NT * wn + j) + (lane & 15);
-    if (row >= p.n) continue;
 #pragma unroll
     for (int i = 0; i < KT; ++i)
-      store_sums(p.dw + static_cast<int64_t>(row) * p.k, k0 + 16 * (KT * wk + i) + 4 * (lane >> 4), p.k, acc[i][j],
-                     p.add != 0);
+      *reinterpret_cast<f32x4_t*>(mine + (lane & 15) * kRow + 4 * (16 * i + 4 * (lane >> 4))) = acc[i][j];
+    fence();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = 2 * i + (lane >> 5), row = n0 + 16 * (NT * wn + j) + at;
+      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(mine + at * kRow + 16 * (lane & 31));
+      if (row < p.n)
+        store_sums(p.dw + static_cast<int64_t>(row) * p.k, k0 + 128 * wk + 4 * (lane & 31), p.k, v, p.add != 0);
+    }
+    fence();
   }
 }
 
@@ -1042,40 +1063,52 @@ void launch_wgrad_turns(const WgradArgs& p, hipStream_t stream) {
     hipLaunchKernelGGL(wgrad_turns_kernel<kDyOdd>, grid, dim3(512), 0, stream, p);
 }
 
-// Runs of steps whose partial sums go through the workspace: where even 64 x 64
-// tiles leave most CUs without work and there are many tokens.
-int wgrad_splits(int64_t tokens, int64_t n, int64_t k) {
-  const int64_t tiles = tiles_of(n, k, 64, 64), steps = (tokens + kTokens - 1) / kTokens;
-  return static_cast<int>(std::max<int64_t>(1, std::min(512 / tiles, steps / 4)));
+// Which kernel, and over how many runs of tokens whose partial sums go through
+// the workspace: the least of these estimates of its time in microseconds.  Per
+// step of 64 tokens, measured with enough steps: 64 x 64 tiles 0.45 while there
+// are few workgroups and 0.12 + 1 / 1050 each then (625: 0.75, 4096: 3.6);
+// 128 x 128 tiles 0.9 and from 360 on 1 / 400 each (169: 0.91, 1024: 2.6);
+// 256 x 256 tiles 1.7 a round of 256 (256: 1.7).  Partial sums cost their
+// traffic at 4.5 TB/s and a launch.
+struct WgradPlan {
+  int tile, splits, split_steps;
+};
+WgradPlan wgrad_plan(int64_t tokens, int64_t n, int64_t k) {
+  const int64_t steps = (tokens + kTokens - 1) / kTokens;
+  const int64_t t64 = tiles_of(n, k, 64, 64), t128 = tiles_of(n, k, 128, 128), t256 = tiles_of(n, k, 256, 256);
+  WgradPlan best{256, 1, static_cast<int>(steps)};
+  double least = n >= 8 ? 10 + 1.7 * static_cast<double>(steps) * static_cast<double>((t256 + 255) / 256) : 1e30;
+  for (int splits = 1; splits <= 32 && (splits == 1 || splits * 4 <= steps); ++splits) {
+    const int64_t each = (steps + splits - 1) / splits;
+    if ((steps + each - 1) / each != splits) continue;
+    const double sums = splits == 1 ? 0 : 3 + (2 * splits + 1) * 4e-6 / 4.5 * static_cast<double>(n * k);
+    const double s = static_cast<double>(each), w64 = static_cast<double>(t64 * splits),
+                 w128 = static_cast<double>(t128 * splits);
+    const double us64 = 3 + s * std::max(0.45, 0.12 + w64 / 1050) + sums;
+    const double us128 = 4 + s * std::max(0.9, w128 / 400) + sums;
+    if (us64 < least) least = us64, best = {64, splits, static_cast<int>(each)};
+    if (us128 < least) least = us128, best = {128, splits, static_cast<int>(each)};
+  }
+  return best;
 }
 
 void launch_wgrad(const WgradArgs& args, float* workspace, hipStream_t stream) {
+  const WgradPlan plan = wgrad_plan(args.tokens, args.n, args.k);
   WgradArgs p = args;
-  const int steps = (p.tokens + kTokens - 1) / kTokens;
-  p.splits = 1;
-  p.split_steps = steps;
-#ifdef FORCEW
-  switch (FORCEW) {
-    case 0: launch_wgrad_turns(p, stream); return;
-    case 1: launch_wgrad_tiles<4, 4, 2, 2>(p, stream); return;
-    case 2: launch_wgrad_tiles<2, 2, 2, 2>(p, stream); return;
-  }
-#endif
-  const int splits = wgrad_splits(p.tokens, p.n, p.k);
-  if (splits > 1) {
-    p.split_steps = (steps + splits - 1) / splits;
-    p.splits = (steps + p.split_steps - 1) / p.split_steps;
+  p.splits = plan.splits;
+  p.split_steps = plan.split_steps;
+  if (plan.splits > 1) {
     p.dw = workspace;
     p.add = 0;
-    launch_wgrad_tiles<2, 2, 2, 2>(p, stream);
-    launch_partial_sums(workspace, static_cast<int64_t>(p.n) * p.k, p.splits, args.dw, args.add, stream);
-  } else if (tiles_of(p.n, p.k, 64, 64) <= 1024) {
-    launch_wgrad_tiles<2, 2, 2, 2>(p, stream);
-  } else if (tiles_of(p.n, p.k, 256, 256) < 192) {
-    launch_wgrad_tiles<4, 4, 2, 2>(p, stream);
-  } else {
-    launch_wgrad_turns(p, stream);
   }
+  if (plan.tile == 64)
+    launch_wgrad_tiles<2, 2, 2, 2>(p, stream);
+  else if (plan.tile == 128)
+    launch_wgrad_tiles<4, 4, 2, 2>(p, stream);
+  else
+    launch_wgrad_turns(p, stream);
+  if (plan.splits > 1)
+    launch_partial_sums(workspace, static_cast<int64_t>(p.n) * p.k, p.splits, args.dw, args.add, stream);
 }
 
 }  // namespace
@@ -1111,7 +1144,7 @@ taco_status_t taco_matmul_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_
 
 size_t taco_wgrad_fp8_workspace_bytes(int64_t tokens, int64_t n, int64_t k) {
   if (!matrix_ok(tokens, n) || !matrix_ok(tokens, k) || !matrix_ok(n, k)) return 0;
-  const int splits = wgrad_splits(tokens, n, k);
+  const int splits = wgrad_plan(tokens, n, k).splits;
   return splits > 1 ? static_cast<size_t>(4 * n * k) * splits : 0;
 }
 
