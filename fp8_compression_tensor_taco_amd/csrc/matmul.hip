@@ -195,7 +195,9 @@ struct MatmulTile {
   static_assert(16 * NT <= kBlock && kBlock % (16 * NT) == 0, "a wavefront's rows of b share their scale");
   static_assert(16 * MT <= 64, "a lane per row of a in a copy of scales");
   static_assert(S >= 2 && S - 2 <= kPeriod, "the next scales are older than the S - 2 newest steps when they are due");
-  static_assert((KG - 1) * kGroup * NT * MT * 1024 <= kLds, "the groups' sums fit where the operands were");
+  static constexpr int kSums = (KG - 1) * kGroup * NT * MT * 1024;                // at the end: the groups' sums,
+  static constexpr int kRow = 2 * BN + 16;                                        // then rows of bf16, bank groups apart
+  static_assert(kSums + BM * kRow <= kLds, "they fit where the operands were");
 };
 
 template <int NT, int MT, int WN, int WM, int KG, int S>
@@ -287,33 +289,49 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void matmul_tiles_kernel(
     }
     slot = slot + 1 == S ? 0 : slot + 1;
   }
+  __syncthreads();
   if constexpr (KG > 1) {
     f32x4_t* sums = reinterpret_cast<f32x4_t*>(lds);      // [group - 1][wavefront][tile][lane]
-    __syncthreads();
     if (group > 0) {
 #pragma unroll
       for (int i = 0; i < NT * MT; ++i) sums[(((group - 1) * T::kGroup + wave) * NT * MT + i) * 64 + lane] = (&acc[0][0])[i];
     }
     __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int q = 0; q < KG - 1; ++q)
+#pragma unroll
+        for (int i = 0; i < NT * MT; ++i) (&acc[0][0])[i] += sums[((q * T::kGroup + wave) * NT * MT + i) * 64 + lane];
+    }
+  }
+  if (partial != nullptr) {
     if (group > 0) return;
 #pragma unroll
-    for (int q = 0; q < KG - 1; ++q)
-#pragma unroll
-      for (int i = 0; i < NT * MT; ++i) (&acc[0][0])[i] += sums[((q * T::kGroup + wave) * NT * MT + i) * 64 + lane];
-  }
-#pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int row = m0 + 16 * (MT * wm + j) + r;
-    if (row >= m) continue;
-    if (partial != nullptr) {
+    for (int j = 0; j < MT; ++j) {
+      const int row = m0 + 16 * (MT * wm + j) + r;
+      if (row >= m) continue;
       float* out = partial + (static_cast<int64_t>(blockIdx.y) * m + row) * n;
 #pragma unroll
       for (int i = 0; i < NT; ++i) store_sums(out, n0 + 16 * (NT * wn + i) + 4 * g, n, acc[i][j], false);
-      continue;
     }
-    uint16_t* out = y + static_cast<int64_t>(row) * n;
+    return;
+  }
+  // The tile goes through LDS, so that whole rows of it are stored.
+  uint8_t* rows = lds + T::kSums;
+  if (group == 0) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) store_columns(out, n0 + 16 * (NT * wn + i) + 4 * g, n, acc[i][j]);
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        *reinterpret_cast<uint2*>(rows + (16 * (MT * wm + j) + r) * T::kRow + 2 * (16 * (NT * wn + i) + 4 * g)) =
+            make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < T::BM * T::BN / 8; p += T::kThreads) {
+    const int row = p / (T::BN / 8), c = p % (T::BN / 8);
+    if (m0 + row < m)
+      store_chunk<false>(y + static_cast<int64_t>(m0 + row) * n, n0 + 8 * c, n,
+                         *reinterpret_cast<const uint4*>(rows + row * T::kRow + 16 * c));
   }
 }
 
