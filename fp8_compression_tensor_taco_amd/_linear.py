@@ -13,7 +13,7 @@ import ctypes
 
 import torch
 
-from ._binding import _check, _on, _workspace, load
+from ._binding import _check, _on, load
 
 BLOCK = 128
 
@@ -103,16 +103,18 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _scratch(workspace, device, nbytes, kind, handle):
-    """(pointer, bytes) of the given workspace, or of the binding's own; none where 0 bytes are needed."""
-    if workspace is not None:
-        if not workspace.is_contiguous() or workspace.device != device:
-            raise ValueError(f"workspace must be contiguous and on {device}")
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    if nbytes == 0:
-        return None, 0
-    ws = _workspace(device, nbytes, kind, handle)
-    return ws.data_ptr(), ws.numel()
+def _scratch(workspace, device, nbytes):
+    """(the given workspace or a new one, its address, its bytes).
+
+    A new one per call: torch's allocator hands it out again in the stream's
+    order, and a captured graph keeps its own."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
+    elif not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 # Every call with a stream makes it current and calls itself: outputs, copies of
@@ -210,10 +212,10 @@ def rmsnorm_backward(dy: torch.Tensor, z: torch.Tensor, rstd: torch.Tensor, weig
         dz = _shaped(dz, "dz", torch.bfloat16, (tokens, hidden), dev)
     dx = _output(dx, "dx", torch.bfloat16, (tokens, hidden), dev)
     dweight = _output(dweight, "dweight", torch.float32, (hidden,), dev)
-    lib, handle = _lib(), _current(dev)
-    ws = _scratch(workspace, dev, lib.taco_rmsnorm_backward_workspace_bytes(tokens, hidden), "rmsnorm_backward", handle)
+    lib = _lib()
+    workspace, at, size = _scratch(workspace, dev, lib.taco_rmsnorm_backward_workspace_bytes(tokens, hidden))
     _check(lib.taco_rmsnorm_backward(dy.data_ptr(), z.data_ptr(), rstd.data_ptr(), weight.data_ptr(), _ptr(dz),
-                                     tokens, hidden, dx.data_ptr(), dweight.data_ptr(), *ws, handle))
+                                     tokens, hidden, dx.data_ptr(), dweight.data_ptr(), at, size, _current(dev)))
     return dx, dweight
 
 
@@ -237,10 +239,10 @@ def matmul_fp8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.T
     if qb.device != dev:
         raise ValueError("all tensors must be on the same device")
     out = _output(out, "out", torch.bfloat16, (m, n), dev)
-    lib, handle = _lib(), _current(dev)
-    ws = _scratch(workspace, dev, lib.taco_matmul_fp8_workspace_bytes(m, n, k), "matmul_fp8", handle)
+    lib = _lib()
+    workspace, at, size = _scratch(workspace, dev, lib.taco_matmul_fp8_workspace_bytes(m, n, k))
     _check(lib.taco_matmul_fp8(qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(), m, n, k,
-                               out.data_ptr(), *ws, handle))
+                               out.data_ptr(), at, size, _current(dev)))
     return out
 
 
@@ -261,10 +263,10 @@ def wgrad_fp8(dy: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, cols: int,
     if accumulate and dw is None:
         raise ValueError("accumulate=True adds to dw: pass it")
     dw = _output(dw, "dw", torch.float32, (n, cols), dev)
-    lib, handle = _lib(), _current(dev)
-    ws = _scratch(workspace, dev, lib.taco_wgrad_fp8_workspace_bytes(tokens, n, cols), "wgrad_fp8", handle)
+    lib = _lib()
+    workspace, at, size = _scratch(workspace, dev, lib.taco_wgrad_fp8_workspace_bytes(tokens, n, cols))
     _check(lib.taco_wgrad_fp8(dy.data_ptr(), q.data_ptr(), scale.data_ptr(), tokens, n, cols, dw.data_ptr(),
-                              int(bool(accumulate)), *ws, handle))
+                              int(bool(accumulate)), at, size, _current(dev)))
     return dw
 
 

@@ -211,6 +211,11 @@ __global__ __launch_bounds__(RowGroup<WPR>::kWG) void rmsnorm_quantize_kernel(
 // `partial`, and column_sums_kernel adds the workgroups' rows in order.  Two
 // rows at a time and two or more workgroups per CU keep the loads going across
 // the rows' reductions.
+//
+// The multiply-adds are written out, so that a row's result does not depend on
+// its place or on the kernel that computes it.
+__device__ __forceinline__ float norm_gradient(float g, float xhat, float mean) { return fmaf(-xhat, mean, g); }
+
 template <int WAVES, int CH, int R, bool WIDE>
 __global__ __launch_bounds__(64 * WAVES) void rmsnorm_backward_kernel(
     const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, const float* __restrict__ rstd,
@@ -280,12 +285,11 @@ __global__ __launch_bounds__(64 * WAVES) void rmsnorm_backward_kernel(
         unpack8(x[k][i], b);
         unpack8(w[i], ww);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[j] = r[k] * (a[j] * ww[j] - b[j] * r[k] * sum);
-        if (dz != nullptr) {
-          unpack8(add[k][i], b);
+        for (int j = 0; j < 8; ++j) a[j] = norm_gradient(a[j] * ww[j], b[j] * r[k], sum);
+        float add_to[8] = {};
+        if (dz != nullptr) unpack8(add[k][i], add_to);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) a[j] += b[j];
-        }
+        for (int j = 0; j < 8; ++j) a[j] = fmaf(r[k], a[j], add_to[j]);
         store_chunk<WIDE>(dx + (row0 + k) * cols, column(i), cols, pack8(a));
       }
     }
@@ -340,7 +344,7 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_backward_long_kernel(
     for (int j = 0; j < 8; ++j) {
       const float xhat = b[j] * r;
       acc[j] = fmaf(a[j], xhat, acc[j]);
-      v[j] += r * (a[j] * ww[j] - xhat * c);
+      v[j] = fmaf(r, norm_gradient(a[j] * ww[j], xhat, c), v[j]);
     }
     store_chunk<WIDE>(dx + row * cols, col, cols, pack8(v));
   }
@@ -432,7 +436,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_quantize_kernel(const uint16_
 
 __device__ __forceinline__ void swiglu_gradient(float dh, float g, float u, float& dg, float& du) {
   const float s = sigmoid(g);
-  dg = dh * u * s * (1.0f + g * (1.0f - s));
+  dg = dh * u * s * fmaf(g, 1.0f - s, 1.0f);
   du = dh * g * s;
 }
 
