@@ -35,20 +35,24 @@ from ._linear import (  # noqa: F401
     fp8_cols,
     fp8_scale_cols,
     matmul_fp8,
+    matmul_fp8_workspace_bytes,
     quantize_rows,
     quantize_weight,
     rmsnorm_backward,
+    rmsnorm_backward_workspace_bytes,
     rmsnorm_quantize,
     swiglu_backward,
     swiglu_quantize,
     wgrad_fp8,
+    wgrad_fp8_workspace_bytes,
 )
 
 __all__ = [
     "TACO_AMAX_FLOATS", "TACO_AMAX_SLOTS", "TACO_DEFAULT_BARRIER_POLLS", "TACO_FLAG_TWO_PASS", "TACO_MAX_PARTS",
     "TacoError", "compress", "compress_blockscale", "compress_delayed", "compress_int8", "compress_noalloc", "decompress",
     "decompress_blockscale", "decompress_int8", "decompress_sum", "decompress_sum_compress", "fp8_cols",
-    "fp8_scale_cols", "is_single_pass", "library_path", "load", "matmul_fp8", "num_scales", "quantize_rows",
-    "quantize_weight", "rmsnorm_backward", "rmsnorm_quantize", "swiglu_backward", "swiglu_quantize",
-    "two_shot_allreduce", "version", "wgrad_fp8", "workspace_bytes", "workspace_timed_out",
+    "fp8_scale_cols", "is_single_pass", "library_path", "load", "matmul_fp8", "matmul_fp8_workspace_bytes",
+    "num_scales", "quantize_rows", "quantize_weight", "rmsnorm_backward", "rmsnorm_backward_workspace_bytes",
+    "rmsnorm_quantize", "swiglu_backward", "swiglu_quantize", "two_shot_allreduce", "version", "wgrad_fp8",
+    "wgrad_fp8_workspace_bytes", "workspace_bytes", "workspace_timed_out",
 ]

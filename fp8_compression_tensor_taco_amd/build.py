@@ -1,4 +1,4 @@
-"""Build libtaco.so (HIP, gfx950) in-tree with hipcc.
+"""Build libtaco.so (HIP, gfx950) in-tree with hipcc, and the torch binding of its 8-bit linear layer.
 
 Usage: ``python -m fp8_compression_tensor_taco_amd.build`` or ``build_library()``.
 """
@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = [os.path.join(CSRC, "taco.hip")]                  # the compression calls (include/taco.h)
 LINEAR_SOURCES = [os.path.join(CSRC, "rowops.hip"),         # the 8-bit linear layer (include/taco_linear.h)
                   os.path.join(CSRC, "matmul.hip")]
+BINDING_SOURCE = os.path.join(CSRC, "linear_binding.cpp")   # host code only
+BINDING_PATH = os.path.join(PKG_DIR, "_linear_binding.so")
 ARCH = "gfx950"
 
 
@@ -44,17 +46,39 @@ def compile_flags() -> list[str]:
 
 
 def build_library(verbose: bool = True) -> str:
-    """Compile every HIP source into ``libtaco.so`` next to this file; returns its path."""
+    """Compile every HIP source into ``libtaco.so`` next to this file, and the binding; returns the library's path."""
     tmp = LIB_PATH + ".tmp"
     cmd = [hipcc(), *compile_flags(), "-shared", "-parallel-jobs=3", *SOURCES, *LINEAR_SOURCES, "-o", tmp]
+    _run(cmd, verbose)
+    os.replace(tmp, LIB_PATH)
+    build_binding(verbose)
+    return LIB_PATH
+
+
+def build_binding(verbose: bool = True) -> str:
+    """Compile ``_linear_binding.so`` against torch and the library beside it; returns its path."""
+    import sysconfig
+
+    from torch.utils import cpp_extension
+
+    tmp = BINDING_PATH + ".tmp"
+    includes = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths()]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
+           *(f"-I{i}" for i in includes), BINDING_SOURCE, "-o", tmp, f"-L{PKG_DIR}", f"-l:{LIB_NAME}",
+           "-Wl,-rpath,$ORIGIN", *(f"-L{i}" for i in cpp_extension.library_paths()), "-ltorch_python", "-ltorch_cpu",
+           "-lc10"]
+    _run(cmd, verbose)
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
+def _run(cmd: list[str], verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError(f"hipcc failed with exit code {res.returncode}")
-    os.replace(tmp, LIB_PATH)
-    return LIB_PATH
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed with exit code {res.returncode}")
 
 
 def build_asm(out_path: str) -> None:

@@ -561,19 +561,22 @@ __global__ __launch_bounds__(512) void matmul_turns_kernel(
   // whole rows of 256 bytes and not 16 pieces of 32.
   constexpr int kRow = 256 + 16;                   // bytes, apart by a bank group
   __syncthreads();
+  int thread = threadIdx.x;
+  opaque(thread);                                  // not kept in registers over the loop
+  const int er = thread & 15, eg = thread >> 4 & 3;
   uint8_t* mine = lds + wave * (64 * kRow);
 #pragma unroll
   for (int j = 0; j < MT; ++j)
 #pragma unroll
     for (int i = 0; i < NT; ++i)
-      *reinterpret_cast<uint2*>(mine + (16 * j + r) * kRow + 2 * (16 * i + 4 * g)) =
+      *reinterpret_cast<uint2*>(mine + (16 * j + er) * kRow + 2 * (16 * i + 4 * eg)) =
           make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
-  const int col = n0 + 128 * wn + 8 * r;
+  fence();
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const int row = m0 + 64 * wm + 4 * i + g;
-    const uint4 v = *reinterpret_cast<const uint4*>(mine + (4 * i + g) * kRow + 16 * r);
-    if (row < m) store_chunk<false>(y + static_cast<int64_t>(row) * n, col, n, v);
+    const int row = m0 + 64 * wm + 4 * i + eg;
+    const uint4 v = *reinterpret_cast<const uint4*>(mine + (4 * i + eg) * kRow + 16 * er);
+    if (row < m) store_chunk<false>(y + static_cast<int64_t>(row) * n, n0 + 128 * wn + 8 * er, n, v);
   }
 }
 
