@@ -741,11 +741,52 @@ struct WgradArgs {
   int splits, split_steps;                       // partial sums over runs of split_steps steps, at dw + split * n * k
 };
 
-// Tiles of BN = 16 NT WN rows by BK = 16 KT WK columns of dw, two steps in LDS,
-// the next one's global loads in registers.
+// Whole steps of 64 tokens on their way from memory to LDS: a thread's pieces
+// are a fixed number of rows apart, so an operand needs one offset, and no row
+// is checked.
+template <int BK, int BN, int THREADS, DyRows ROWS>
+struct StepMover {
+  using X = XPart<BK, THREADS>;
+  using D = DyPart<BN, THREADS, ROWS>;
+  static constexpr int kRowsD = kTokens / D::N, kRowsX = kTokens / X::N;       // between a thread's pieces
+  static_assert(kRowsD % 16 == 0 && kRowsX % 16 == 0, "rows that far apart have the same swizzle");
+  unsigned from_d, from_q, from_s;
+  int to_d, to_x, drop;
+  __device__ __forceinline__ StepMover(const WgradArgs& p, int thread, int n0, int k0) {
+    const int row_d = thread / (BN / 8), piece_d = thread % (BN / 8), col_d = n0 + 8 * piece_d;
+    const int row_x = thread / (BK / 16), piece_x = thread % (BK / 16), col_x = min(k0 + 16 * piece_x, p.kcols - 16);
+    from_d = 2 * (row_d * p.n + min(col_d, p.n - 8));
+    from_q = row_x * p.kcols + col_x;
+    from_s = row_x * p.kscales + col_x / kBlock;
+    to_d = TokenTile<BN>::at(row_d, piece_d >> 1) + 16 * (piece_d & 1);
+    to_x = TokenTile<BK>::at(row_x, piece_x);
+    drop = min(max(col_d - (p.n - 8), 0), 7);
+  }
+  // Piece i of the step that starts at token t.
+  __device__ __forceinline__ void load_d(const WgradArgs& p, int64_t t, int i, D& d) const {
+    d.v[i] = load16_at(uniform(reinterpret_cast<const uint8_t*>(p.dy + (t + i * kRowsD) * p.n)), from_d);
+  }
+  __device__ __forceinline__ void load_x(const WgradArgs& p, int64_t t, int i, X& x) const {
+    x.v[i] = load16_at(uniform(p.q + (t + i * kRowsX) * p.kcols), from_q);
+    x.byte[i] = load1_at(uniform(p.scale + (t + i * kRowsX) * p.kscales), from_s);
+  }
+  __device__ __forceinline__ void store_d(uint8_t* tile, int i, const D& d) const {
+    *reinterpret_cast<uint4*>(tile + to_d + i * kRowsD * TokenTile<BN>::kRow) =
+        ROWS == kDyOdd ? drop_elements(d.v[i], drop) : d.v[i];
+  }
+  __device__ __forceinline__ void store_x(uint8_t* tile, int i, const X& x) const {
+    widen16(x.v[i], x.byte[i], reinterpret_cast<uint4*>(tile + to_x + i * kRowsX * TokenTile<BK>::kRow));
+  }
+};
+
+// Tiles of BN = 16 NT WN rows by BK = 16 KT WK columns of dw, two steps in LDS
+// and the global loads of the next two in registers.  Eight wavefronts for 128 x
+// 128: a step of one workgroup per CU waits less with two wavefronts per SIMD
+// than with one (1021 x 1600 x 1600: 15.6 against 17.4 us).
 template <int KT, int NT, int WK, int WN, DyRows ROWS>
 __global__ __launch_bounds__(64 * WK * WN) void wgrad_tiles_kernel(const WgradArgs p) {
   constexpr int BK = 16 * KT * WK, BN = 16 * NT * WN, kThreads = 64 * WK * WN;
+  using Mover = StepMover<BK, BN, kThreads, ROWS>;
   using X = TokenTile<BK>;
   using D = TokenTile<BN>;
   __shared__ __align__(256) uint8_t lds[2 * (X::kBytes + D::kBytes)];
@@ -759,22 +800,17 @@ __global__ __launch_bounds__(64 * WK * WN) void wgrad_tiles_kernel(const WgradAr
   const int last = min(p.tokens, first + p.split_steps * kTokens);
   const int wk = wave % WK, wn = wave / WK;
   const int off_x = read_offset<BK>(lane, KT * wk), off_d = read_offset<BN>(lane, NT * wn);
-  XPart<BK, kThreads> x;
-  DyPart<BN, kThreads, ROWS> d;
+  const Mover mover(p, threadIdx.x, n0, k0);
+  typename Mover::X x[2];
+  typename Mover::D d[2];
   f32x4_t acc[KT][NT] = {};
-  x.load(threadIdx.x, p.q, p.scale, first, last, k0, p.kcols, p.kscales);
-  d.load(threadIdx.x, p.dy, first, last, n0, p.n);
-  int buf = 0;
-  for (int t0 = first; t0 < last; t0 += kTokens, buf ^= 1) {
-    uint8_t* tx = lds + buf * X::kBytes;
-    uint8_t* td = lds + 2 * X::kBytes + buf * D::kBytes;
-    x.store(threadIdx.x, tx, t0, last);
-    d.store(threadIdx.x, td, t0, last, n0, p.n);
-    if (t0 + kTokens < last) {
-      x.load(threadIdx.x, p.q, p.scale, t0 + kTokens, last, k0, p.kcols, p.kscales);
-      d.load(threadIdx.x, p.dy, t0 + kTokens, last, n0, p.n);
-    }
-    reads_done_and_meet();
+  auto load = [&](int t0, auto set) {
+#pragma unroll
+    for (int i = 0; i < Mover::D::N; ++i) mover.load_d(p, t0, i, d[set]);
+#pragma unroll
+    for (int i = 0; i < Mover::X::N; ++i) mover.load_x(p, t0, i, x[set]);
+  };
+  auto products = [&](const uint8_t* tx, const uint8_t* td) {
 #pragma unroll
     for (int c = 0; c < kTokens / 32; ++c) {
       bf16x8_t fx[KT], fd[NT];
@@ -784,6 +820,35 @@ __global__ __launch_bounds__(64 * WK * WN) void wgrad_tiles_kernel(const WgradAr
       for (int j = 0; j < NT; ++j) fd[j] = read_columns<BN>(td, off_d, j, c);
       multiply(fx, fd, acc, [](int) {});
     }
+  };
+  const int whole = ROWS == kDyShort ? first : first + (last - first) / kTokens * kTokens;   // end of the whole steps
+  auto step = [&](int t0, auto set) {
+    uint8_t* tx = lds + set * X::kBytes;
+    uint8_t* td = lds + 2 * X::kBytes + set * D::kBytes;
+#pragma unroll
+    for (int i = 0; i < Mover::D::N; ++i) mover.store_d(td, i, d[set]);
+#pragma unroll
+    for (int i = 0; i < Mover::X::N; ++i) mover.store_x(tx, i, x[set]);
+    if (t0 + 2 * kTokens < whole) load(t0 + 2 * kTokens, set);
+    reads_done_and_meet();
+    products(tx, td);
+  };
+  constexpr std::integral_constant<int, 0> zero{};
+  constexpr std::integral_constant<int, 1> one{};
+  if (first < whole) load(first, zero);
+  if (first + kTokens < whole) load(first + kTokens, one);
+  for (int t0 = first; t0 < whole; t0 += 2 * kTokens) {
+    step(t0, zero);
+    if (t0 + kTokens < whole) step(t0 + kTokens, one);
+  }
+  for (int t0 = whole; t0 < last; t0 += kTokens) {               // what is left over; all of it where rows are short
+    x[0].load(threadIdx.x, p.q, p.scale, t0, last, k0, p.kcols, p.kscales);
+    d[0].load(threadIdx.x, p.dy, t0, last, n0, p.n);
+    __syncthreads();
+    x[0].store(threadIdx.x, lds, t0, last);
+    d[0].store(threadIdx.x, lds + 2 * X::kBytes, t0, last, n0, p.n);
+    __syncthreads();
+    products(lds, lds + 2 * X::kBytes);
   }
   float* out = p.dw + static_cast<int64_t>(blockIdx.y) * p.n * p.k;
 #pragma unroll
@@ -793,7 +858,7 @@ __global__ __launch_bounds__(64 * WK * WN) void wgrad_tiles_kernel(const WgradAr
 #pragma unroll
     for (int i = 0; i < KT; ++i)
       store_sums(out + static_cast<int64_t>(row) * p.k, k0 + 16 * (KT * wk + i) + 4 * (lane >> 4), p.k, acc[i][j],
-                     p.add != 0);
+                 p.add != 0);
   }
 }
 
@@ -814,10 +879,9 @@ template <DyRows ROWS>
 __global__ __launch_bounds__(512) void wgrad_turns_kernel(const WgradArgs p) {
   constexpr int KT = 8, NT = 4, B = 256, kThreads = 512;
   using Tile = TokenTile<B>;
-  using D = DyPart<B, kThreads, ROWS>;
-  using X = XPart<B, kThreads>;
-  constexpr int kRowsD = kTokens / D::N, kRowsX = kTokens / X::N;     // between a thread's pieces
-  static_assert(kRowsD % 16 == 0 && kRowsX % 16 == 0, "rows that far apart have the same swizzle");
+  using Mover = StepMover<B, B, kThreads, ROWS>;
+  using D = typename Mover::D;
+  using X = typename Mover::X;
   __shared__ __align__(256) uint8_t lds[4 * Tile::kBytes];           // x, x, dy, dy
   const int lane = threadIdx.x & 63, thread = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -828,32 +892,16 @@ __global__ __launch_bounds__(512) void wgrad_turns_kernel(const WgradArgs p) {
   const int wk = wave & 1, wn = wave >> 1;
   int off_x = read_offset<B>(lane, KT * wk), off_d = read_offset<B>(lane, NT * wn);
 
-  const int col_d = n0 + 8 * (thread & 31), col_x = min(k0 + 16 * (thread & 15), p.kcols - 16);
-  const unsigned from_d = 2 * ((thread >> 5) * p.n + min(col_d, p.n - 8));
-  const unsigned from_q = (thread >> 4) * p.kcols + col_x, from_s = (thread >> 4) * p.kscales + col_x / kBlock;
-  const int to_d = Tile::at(thread >> 5, (thread & 31) >> 1) + 16 * (thread & 1);
-  const int to_x = Tile::at(thread >> 4, thread & 15);
-  const int drop = min(max(col_d - (p.n - 8), 0), 7);
+  const Mover mover(p, thread, n0, k0);
   const int steps = p.tokens / kTokens;
   D d;
   X x;
   // past the last step the last one is read again, into a buffer nobody reads
-  auto load_d = [&](int s, int i) {
-    const int64_t t = static_cast<int64_t>(min(s, steps - 1)) * kTokens + i * kRowsD;
-    d.v[i] = load16_at(uniform(reinterpret_cast<const uint8_t*>(p.dy + t * p.n)), from_d);
-  };
-  auto load_x = [&](int s, int i) {
-    const int64_t t = static_cast<int64_t>(min(s, steps - 1)) * kTokens + i * kRowsX;
-    x.v[i] = load16_at(uniform(p.q + t * p.kcols), from_q);
-    x.byte[i] = load1_at(uniform(p.scale + t * p.kscales), from_s);
-  };
-  auto store_d = [&](int buf, int i) {
-    *reinterpret_cast<uint4*>(lds + (2 + buf) * Tile::kBytes + to_d + i * kRowsD * Tile::kRow) =
-        ROWS == kDyOdd ? drop_elements(d.v[i], drop) : d.v[i];
-  };
-  auto store_x = [&](int buf, int i) {
-    widen16(x.v[i], x.byte[i], reinterpret_cast<uint4*>(lds + buf * Tile::kBytes + to_x + i * kRowsX * Tile::kRow));
-  };
+  auto token = [&](int s) { return static_cast<int64_t>(min(s, steps - 1)) * kTokens; };
+  auto load_d = [&](int s, int i) { mover.load_d(p, token(s), i, d); };
+  auto load_x = [&](int s, int i) { mover.load_x(p, token(s), i, x); };
+  auto store_d = [&](int buf, int i) { mover.store_d(lds + (2 + buf) * Tile::kBytes, i, d); };
+  auto store_x = [&](int buf, int i) { mover.store_x(lds + buf * Tile::kBytes, i, x); };
   f32x4_t acc[KT][NT] = {};
   auto read = [&](int buf, int c, bf16x8_t (&fx)[KT], bf16x8_t (&fd)[NT]) {
 #pragma unroll
@@ -1086,10 +1134,10 @@ void launch_wgrad_turns(const WgradArgs& p, hipStream_t stream) {
 
 // Which kernel, and over how many runs of tokens whose partial sums go through
 // the workspace: the least of these estimates of its time in microseconds.  Per
-// step of 64 tokens, measured with enough steps: 64 x 64 tiles 0.45 while there
-// are few workgroups and 0.12 + 1 / 1050 each then (625: 0.75, 4096: 3.6);
-// 128 x 128 tiles 0.9 and from 360 on 1 / 400 each (169: 0.91, 1024: 2.6);
-// 256 x 256 tiles 1.7 a round of 256 (256: 1.7).  Partial sums cost their
+// step of 64 tokens, measured: 64 x 64 tiles 0.37 while there are few
+// workgroups and 0.12 + 1 / 1050 each then (169: 0.37, 650: 0.75, 1024: 1.05,
+// 4096: 3.6); 128 x 128 tiles 0.65 and from 254 on 1 / 390 each (169: 0.63, 256:
+// 0.75, 650: 1.7); 256 x 256 tiles 1.7 a round of 256.  Partial sums cost their
 // traffic at 4.5 TB/s and a launch.
 struct WgradPlan {
   int tile, splits, split_steps;
@@ -1105,8 +1153,8 @@ WgradPlan wgrad_plan(int64_t tokens, int64_t n, int64_t k) {
     const double sums = splits == 1 ? 0 : 3 + (2 * splits + 1) * 4e-6 / 4.5 * static_cast<double>(n * k);
     const double s = static_cast<double>(each), w64 = static_cast<double>(t64 * splits),
                  w128 = static_cast<double>(t128 * splits);
-    const double us64 = 3 + s * std::max(0.45, 0.12 + w64 / 1050) + sums;
-    const double us128 = 4 + s * std::max(0.9, w128 / 400) + sums;
+    const double us64 = 3 + s * std::max(0.37, 0.12 + w64 / 1050) + sums;
+    const double us128 = 4 + s * std::max(0.65, w128 / 390) + sums;
     if (us64 < least) least = us64, best = {64, splits, static_cast<int>(each)};
     if (us128 < least) least = us128, best = {128, splits, static_cast<int>(each)};
   }
@@ -1125,7 +1173,7 @@ void launch_wgrad(const WgradArgs& args, float* workspace, hipStream_t stream) {
   if (plan.tile == 64)
     launch_wgrad_tiles<2, 2, 2, 2>(p, stream);
   else if (plan.tile == 128)
-    launch_wgrad_tiles<4, 4, 2, 2>(p, stream);
+    launch_wgrad_tiles<4, 2, 2, 4>(p, stream);
   else
     launch_wgrad_turns(p, stream);
   if (plan.splits > 1)
