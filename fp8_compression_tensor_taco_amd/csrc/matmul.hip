@@ -423,11 +423,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void matmul_few_kernel(
 // copies of a wavefront) each.  Copies retire in issue order, so operations
 // issued later only make a wait stricter.
 //
-// 8192 x 8192 x 8192: 383 us, 2.87 PFLOP/s; 8192 x 14336 x 3584: 336 us, 2.51.
-// Without the loop's copies 8192^3 takes 324 us, without the LDS reads 321, the
-// copies alone 206: the two compete for LDS and the barriers cost the rest.
-// With one step in flight (two whole buffers) it took 435 us, with the copies
-// among the matrix instructions 390.
+// 8192 x 8192 x 8192: 375 to 400 us on different cards, 2.75 to 2.9 PFLOP/s;
+// 8192 x 14336 x 3584: 310 to 335 us, 2.5 to 2.7.  A step takes about 1.4 us where
+// its matrix instructions alone take 1.02, a tile's start and end about 4.  When
+// 8192^3 took 383 us it took 324 without the loop's copies, 321 without the LDS
+// reads, and the copies alone 206: the two compete for LDS and the barriers cost
+// the rest.  With one step in flight (two whole buffers) it took 435 us, with the
+// copies among the matrix instructions 390.
 constexpr int kBig = 256;                       // rows of either operand in a tile
 constexpr int kUnit = 128 * kBlock;             // bytes: 128 rows of 128 columns
 constexpr int kRing = 9;
@@ -782,7 +784,9 @@ struct StepMover {
 // Tiles of BN = 16 NT WN rows by BK = 16 KT WK columns of dw, two steps in LDS
 // and the global loads of the next two in registers.  Eight wavefronts for 128 x
 // 128: a step of one workgroup per CU waits less with two wavefronts per SIMD
-// than with one (1021 x 1600 x 1600: 15.6 against 17.4 us).
+// than with one (1021 x 1600 x 1600: 15.6 against 17.4 us).  At that size 169 of
+// 256 CUs have a tile and a step costs 0.65 us, of which the matrix instructions
+// are 0.12: latency.
 template <int KT, int NT, int WK, int WN, DyRows ROWS>
 __global__ __launch_bounds__(64 * WK * WN) void wgrad_tiles_kernel(const WgradArgs p) {
   constexpr int BK = 16 * KT * WK, BN = 16 * NT * WN, kThreads = 64 * WK * WN;
@@ -875,6 +879,9 @@ __global__ __launch_bounds__(64 * WK * WN) void wgrad_tiles_kernel(const WgradAr
 // hold nothing but the reads, and whole steps need no check of rows and one
 // offset per operand (a thread's pieces are a fixed number of rows apart); the
 // rows that are left over follow as one step of their own, without turns.
+// 4096 x 16384 x 4096: 465 to 485 us on different cards, 1.13 to 1.18 PFLOP/s; the
+// stores to LDS account for about 43 us of it, the loads for 80, the end of the
+// tiles for 40.  Loads in M1, or both loads and stores later, made no difference.
 template <DyRows ROWS>
 __global__ __launch_bounds__(512) void wgrad_turns_kernel(const WgradArgs p) {
   constexpr int KT = 8, NT = 4, B = 256, kThreads = 512;
@@ -1079,21 +1086,24 @@ void launch_big(const MatmulArgs& p, hipStream_t stream) {
 
 // Which kernel: by the number of tiles against the 256 CUs.  Measured (us):
 //   m     n     k      64x64 KG 2  64x64 KG 1  128x128 KG 2  128x128 KG 1  256x256
-//   256   4096  4096   10.8        13.1        20.8          25.3          45.8
-//   777   1601  1600   12.2        9.3         13.2          14.6          32.0
-//   512   4096  4096   20.3        16.6        20.9          25.6          46.2
-//   1024  4096  4096   38.8        30.5        22.0          26.1          46.7
-//   2048  4096  4096   76.0        55.6        42.2          35.0          47.9
-//   4096  4096  4096   154         112         107           78.0          59.7
-//   8192  3584  1000   105         58.6        56.1          44.5          42.5
+//   256   4096  4096   10.8        13.4        20.4          24.6          39.1
+//   777   1601  1600   11.3        8.6         10.9          12.4          20.3
+//   512   4096  4096   20.0        16.8        20.6          24.8          39.5
+//   1024  4096  4096   38.4        30.5        21.7          25.5          40.1
+//   2048  4096  4096   75.7        54.4        41.5          33.3          41.6
+//   2816  4096  4096                                         56.6          44.2
+//   4096  4096  4096   153         111         105           75.7          55.1
+//   4608  4096  4096                           106           89.7          87.4
+//   8192  4224  512                            44.9          30.5          33.9
+//   8192  3584  1000   99.4        56.6        50.0          39.2          33.6
 // so 64 x 64 tiles until a CU would have more than three, two groups of
-// wavefronts for a tile where a CU has one.  A round of 256 large tiles takes
-// 1.65 times as long as a round of 512 of 128 x 128, whose leftovers cost less.
+// wavefronts for a tile where a CU has one; 128 x 128 while their workgroups
+// are all resident (two to a CU), and 256 x 256 from there on, which loses up to
+// a tenth where few columns meet a nearly empty last round.
 // Up to 32 rows the direct loads win (16 rows: 6.7 against 9.7, 32: 9.5 against
-// 10.0), and at 64 rows the tiles do (15.2 against 10.6).
+// 10.1), and at 64 rows the tiles do (15.2 against 10.5).
 void launch_matmul(const MatmulArgs& p, hipStream_t stream) {
   const int64_t t64 = tiles_of(p.m, p.n, 64, 64), t128 = tiles_of(p.m, p.n, 128, 128);
-  const int64_t rounds_big = (tiles_of(p.m, p.n, kBig, kBig) + 255) / 256;
   if (p.m <= 16)
     launch_few<1>(p, stream);
   else if (p.m <= 32)
@@ -1107,7 +1117,7 @@ void launch_matmul(const MatmulArgs& p, hipStream_t stream) {
     launch_tiles<2, 2, 2, 2, 1, 3>(p, stream);
   else if (t128 <= 256)
     launch_tiles<4, 4, 2, 2, 2, 2>(p, stream);
-  else if (845 * rounds_big > t128)
+  else if (t128 <= 512)
     launch_tiles<4, 4, 2, 2, 1, 2>(p, stream);
   else
     launch_big(p, stream);

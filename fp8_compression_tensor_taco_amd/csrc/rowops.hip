@@ -7,6 +7,9 @@
 // A lane holds chunks of 8 consecutive columns, 64 lanes 512 consecutive
 // columns, so a wavefront's loads cover 1 KiB and a block of 128 columns sits
 // in 16 consecutive lanes (its maximum takes four DPP rotations).
+//
+// Bandwidths below count each input and output once, over inputs that change
+// from call to call; a copy of 1 GiB moves 5.06 TB/s.
 #include <cmath>
 
 #include <algorithm>
@@ -26,7 +29,10 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // ------------------------------------------------------------------ quantise
 
-// One wavefront for each 512 * CH columns of a row.
+// One wavefront for each 512 * CH columns of a row: no reduction goes beyond 16
+// lanes, so the waves are as many as the CUs can hold and nothing waits but the
+// loads.  4096 x 16384: 43 us, 4.7 TB/s; 8192 x 8191 (element-aligned rows): 42
+// us, 4.7; up to a few hundred KB a launch, 4 us.
 template <int CH, bool WIDE>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t* __restrict__ x, int64_t rows,
                                                                  int cols, int segments, uint8_t* __restrict__ q,
@@ -55,7 +61,8 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t*
 // thread t has columns 8 (t % 16) + 0..7 of rows 8 (t / 16) + 0..7, so a row of
 // the block is read by 16 lanes (256 bytes).  The transpose turns each 8 x 8
 // group of codes in registers and collects whole 128-byte rows in LDS, which
-// leave 16 bytes per lane.
+// leave 16 bytes per lane.  One pass over w for both orders: 14336 x 3584 in
+// 40 us, 5.1 TB/s.
 template <bool WIDE>
 __global__ __launch_bounds__(kThreads) void quantize_weight_kernel(const uint16_t* __restrict__ w, int rows, int cols,
                                                                    uint8_t* __restrict__ q, uint8_t* __restrict__ scale,
@@ -130,6 +137,10 @@ __global__ __launch_bounds__(kThreads) void quantize_weight_kernel(const uint16_
 // WPR wavefronts hold a row, CH chunks per lane; a workgroup is kThreads (rows
 // of one wavefront) or one row.  The row stays in registers as bf16 between
 // the sum of squares and the codes.
+//
+// z = bf16(x + residual), rstd = 1 / sqrt(mean(z^2) + eps), the codes those of
+// z * rstd * weight.  4096 x 4096 with a residual: 24 us, 4.9 TB/s; 8192 x 8000:
+// 85 us, 5.4; 8 x 4096: 5 us, latency.
 template <int WPR>
 struct RowGroup {
   static constexpr int kWG = WPR == 1 ? kThreads : 64 * WPR;
@@ -205,12 +216,15 @@ __global__ __launch_bounds__(RowGroup<WPR>::kWG) void rmsnorm_quantize_kernel(
   pad_scales(sr, chunks / kBlockChunks, static_cast<int>(scols), thread);
 }
 
-// The gradient.  A workgroup of WAVES wavefronts holds R whole rows at a time
+// The gradient, with xhat = z * rstd and mean = sum(dy * weight * xhat) / cols:
+// dx = rstd * (dy * weight - xhat * mean) + dz, dweight = sum over rows of dy * xhat.
+// A workgroup of WAVES wavefronts holds R whole rows at a time
 // (CH chunks per lane and row), walks the rows gridDim.x * R apart and keeps its
 // columns' sums of dy * xhat in registers; it writes them once, as one row of
 // `partial`, and column_sums_kernel adds the workgroups' rows in order.  Two
 // rows at a time and two or more workgroups per CU keep the loads going across
-// the rows' reductions.
+// the rows' reductions.  8192 x 3584: 43 us, 5.5 TB/s, and 5 for the column
+// sums; 1021 x 1600: 6.7 and 3.8, latency.
 //
 // The multiply-adds are written out, so that a row's result does not depend on
 // its place or on the kernel that computes it.
@@ -305,7 +319,9 @@ __global__ __launch_bounds__(64 * WAVES) void rmsnorm_backward_kernel(
 }
 
 // Rows too long for that: first mean(dy * weight * xhat) of each row, a
-// workgroup per row, then the rest by pieces of 2048 columns.
+// workgroup per row, then the rest by pieces of 2048 columns.  dy and z are read
+// twice, the second time mostly from the last-level cache: 1000 x 20000 in 38 us,
+// 3.1 TB/s.
 template <bool WIDE>
 __global__ __launch_bounds__(kThreads) void rmsnorm_row_means_kernel(
     const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, const float* __restrict__ rstd,
@@ -358,7 +374,8 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_backward_long_kernel(
 
 // out[c] = the sum of partial[0..groups)[c]: 16 columns per workgroup, four per
 // lane, 256 row classes.  Many workgroups and few rows each: the sums are in the
-// last-level cache and the reads' latency is the time.
+// last-level cache and the reads' latency is the time: 3.8 us for 511 rows of
+// 1600 columns, 4.9 for 512 of 3584.
 constexpr int kSumClasses = 256;
 __global__ __launch_bounds__(4 * kSumClasses) void column_sums_kernel(const float* __restrict__ partial, int groups,
                                                                       int cols, int64_t stride,
@@ -393,7 +410,9 @@ __global__ __launch_bounds__(4 * kSumClasses) void column_sums_kernel(const floa
 // exp(-g) may be infinite: 1 / (1 + inf) = 0.
 __device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
 
-// One wavefront for each 512 * CH columns of a row's gate and the same of its up part.
+// h = g * sigmoid(g) * u.  One wavefront for each 512 * CH columns of a row's
+// gate and the same of its up part.  4096 tokens, inner 8192: 46 us, 5.1 TB/s;
+// inner 5461 (element-aligned up parts): 41 us, 3.8.
 template <int CH, bool WIDE>
 __global__ __launch_bounds__(kThreads) void swiglu_quantize_kernel(const uint16_t* __restrict__ gu, int64_t rows,
                                                                    int inner, int segments, uint8_t* __restrict__ hq,
@@ -440,8 +459,11 @@ __device__ __forceinline__ void swiglu_gradient(float dh, float g, float u, floa
   du = dh * g * s;
 }
 
+// With s = sigmoid(g): dg = dh * u * s * (1 + g (1 - s)), du = dh * g * s.
+//
 // inner a multiple of 128: the blocks of dgu's columns are blocks of dg or of
-// du, so a lane's chunk of the checkpoint gives a chunk of each.
+// du, so a lane's chunk of the checkpoint gives a chunk of each.  4096 tokens,
+// inner 8192: 62 us, 5.4 TB/s.
 template <int CH>
 __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
     const uint16_t* __restrict__ dh, const uint8_t* __restrict__ cq, const uint8_t* __restrict__ cs, int64_t rows,
@@ -493,7 +515,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
 // Any other inner: a block of dgu's columns may hold the end of dg and the
 // start of du, so a lane computes the 8 output columns it holds: all of dg or
 // all of du, from 8 columns of dh and of the checkpoint at any alignment and in
-// at most two blocks, or, where the two meet and at the end, one by one.
+// at most two blocks, or, where the two meet and at the end, one by one.  It reads
+// dh and the checkpoint twice: 4096 tokens, inner 5440: 68 us, 3.3 TB/s.
 __global__ __launch_bounds__(kThreads) void swiglu_backward_any_kernel(
     const uint16_t* __restrict__ dh, const uint8_t* __restrict__ cq, const uint8_t* __restrict__ cs, int64_t rows,
     int inner, int segments, uint16_t* __restrict__ dgu, uint8_t* __restrict__ dq, uint8_t* __restrict__ ds) {
