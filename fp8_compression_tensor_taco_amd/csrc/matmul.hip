@@ -866,7 +866,34 @@ __global__ __launch_bounds__(64 * WK * WN) void wgrad_tiles_kernel(const WgradAr
   }
 }
 
-// The large gradient: 256 x 256 tiles, two groups of four wavefronts that take
+// A wavefront's 16 NT rows of 128 results.  Sixteen rows at a time go through
+// its part of LDS, so that a store covers two whole rows of 512 bytes and not 16
+// pieces of 64.
+constexpr int kStoreRow = 512 + 16;              // bytes, apart by a bank group
+constexpr int kStoreBytes = 16 * kStoreRow;
+template <int KT, int NT>
+__device__ __forceinline__ void store_wgrad_tile(const WgradArgs& p, uint8_t* mine, int row0, int col0,
+                                                 const f32x4_t (&acc)[KT][NT]) {
+  static_assert(KT == 8, "rows of 128 columns");
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+      *reinterpret_cast<f32x4_t*>(mine + (lane & 15) * kStoreRow + 4 * (16 * i + 4 * (lane >> 4))) = acc[i][j];
+    fence();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = 2 * i + (lane >> 5), row = row0 + 16 * j + at;
+      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(mine + at * kStoreRow + 16 * (lane & 31));
+      if (row < p.n) store_sums(p.dw + static_cast<int64_t>(row) * p.k, col0 + 4 * (lane & 31), p.k, v, p.add != 0);
+    }
+    fence();
+  }
+}
+
+// The large gradient where dy's rows start anywhere (n no multiple of 8), so that
+// they pass through registers: 256 x 256 tiles, two groups of four wavefronts that take
 // turns as in matmul_turns_kernel: while one group multiplies 32 rows of t, the
 // other reads its fragments of 32.  A step of 64 rows has four phases, M0, C0,
 // M1, C1, the second group one behind.  The thread's part of step s + 1 goes
@@ -882,11 +909,10 @@ __global__ __launch_bounds__(64 * WK * WN) void wgrad_tiles_kernel(const WgradAr
 // 4096 x 16384 x 4096: 465 to 485 us on different cards, 1.13 to 1.18 PFLOP/s; the
 // stores to LDS account for about 43 us of it, the loads for 80, the end of the
 // tiles for 40.  Loads in M1, or both loads and stores later, made no difference.
-template <DyRows ROWS>
 __global__ __launch_bounds__(512) void wgrad_turns_kernel(const WgradArgs p) {
   constexpr int KT = 8, NT = 4, B = 256, kThreads = 512;
   using Tile = TokenTile<B>;
-  using Mover = StepMover<B, B, kThreads, ROWS>;
+  using Mover = StepMover<B, B, kThreads, kDyOdd>;
   using D = typename Mover::D;
   using X = typename Mover::X;
   __shared__ __align__(256) uint8_t lds[4 * Tile::kBytes];           // x, x, dy, dy
@@ -981,26 +1007,211 @@ __global__ __launch_bounds__(512) void wgrad_turns_kernel(const WgradArgs p) {
       multiply(fx, fd, acc, [](int) {});
     }
   }
-  // Sixteen rows of 128 results at a time go through LDS, so that a store covers
-  // two whole rows of 512 bytes and not 16 pieces of 64.
-  constexpr int kRow = 512 + 16;                   // bytes, apart by a bank group
   __syncthreads();
-  uint8_t* mine = lds + wave * (16 * kRow);
+  store_wgrad_tile<KT, NT>(p, lds + wave * kStoreBytes, n0 + 16 * NT * wn, k0 + 16 * KT * wk, acc);
+}
+
+// One product into accumulators that stay in the accumulation registers, which
+// the compiler would otherwise move to and from the others around each use.  It
+// does not see a matrix instruction here: accumulators_done() has to stand
+// before anything else reads them, and the operands come straight from LDS reads
+// that were waited for.
+__device__ __forceinline__ void multiply_into(const bf16x8_t& x, const bf16x8_t& d, f32x4_t& acc) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(x), "v"(d));
+#endif
+}
+
+__device__ __forceinline__ void accumulators_done() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
+// All LDS reads of the wavefront are done, known to the compiler as well.
+__device__ __forceinline__ void reads_done() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0), nothing else
+  __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
+// The quantised rows widened to bf16, 16 codes per thread: 4096 x 4096 in 9 us.
+__global__ __launch_bounds__(256) void widen_rows_kernel(const uint8_t* __restrict__ q,
+                                                         const uint8_t* __restrict__ scale, int64_t rows, int kcols,
+                                                         int kscales, uint16_t* __restrict__ out) {
+  const int pieces = kcols / 16;
+  const int64_t p = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, row = p / pieces;
+  if (row >= rows) return;
+  const int c = static_cast<int>(p - row * pieces);
+  widen16(*reinterpret_cast<const uint4*>(q + 16 * p), scale[row * kscales + c / 8],
+          reinterpret_cast<uint4*>(out + 16 * p));
+}
+
+// The large gradient where dy's rows are 16-byte aligned: 256 x 256 tiles, four
+// wavefronts of 128 x 128 each, which read a third less from LDS than eight would; x
+// was widened beforehand, so both operands are copied straight into LDS.
+//
+// A chunk is 32 rows of t, one matrix instruction deep.  Four chunks lie in
+// LDS.  While a wavefront multiplies chunk c it reads its fragments of chunk c + 1
+// between the matrix instructions (dy's into a second set of registers, x's into
+// those whose eight products are done, the last two into a second set) and
+// copies its part of chunk c + 4 over chunk c, which every wavefront holds in registers
+// by then.  One barrier per chunk, before which each wavefront has its reads
+// and its part of chunk c + 2: only the copies of two newer chunks are in flight.
+//
+// 4096 x 16384 x 4096: 418 us with the widening, 1.32 PFLOP/s, against 490 on
+// the same card for wgrad_turns_kernel; 8192 x 8192 x 8192: 803 (1.37) against 942.
+// With the accumulators left to the compiler it takes 473.
+constexpr int kChunk = 32, kChunkRing = 4;
+constexpr int kChunkBytes = kChunk * 512;        // of 256 columns of an operand
+
+__global__ __launch_bounds__(256) void wgrad_copies_kernel(const WgradArgs p, const uint16_t* __restrict__ wide) {
+  constexpr int KT = 8, NT = 8, B = 256, kThreads = 256;
+  constexpr int KR = KT - 2;                       // x fragments read into the registers they were in
+  constexpr int kPair = 4 * kChunkBytes;           // two chunks of both operands
+  using Tile = TokenTile<B>;
+  using D = DyPart<B, kThreads, kDyWhole>;
+  using X = XPart<B, kThreads>;
+  static_assert(kChunkRing == 4 && (kPair & (kPair - 1)) == 0, "the two halves of the ring differ in one address bit");
+  __shared__ __align__(256) uint8_t lds[2 * kPair];
+  const int lane = threadIdx.x & 63, thread = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles_n = (p.n + B - 1) / B, tiles_k = (p.k + B - 1) / B;
+  int tile_n, tile_k;
+  tile_of_block(tiles_n, tiles_k, tile_n, tile_k);
+  const int n0 = tile_n * B, k0 = tile_k * B;
+  const int wk = wave & 1, wn = wave >> 1;
+  const int off_x = read_offset<B>(lane, KT * wk), off_d = read_offset<B>(lane, NT * wn);
+
+  // Copies: a wavefront fills four pairs of rows of each operand, those whose
+  // granules are permuted alike.  Columns past the end are read from the row's
+  // last eight; what they give is never stored.
+  constexpr int kPairs[4] = {0, 2, 8, 10};
+  const int pair0 = (wave & 1) + 4 * (wave >> 1), row0 = 2 * pair0 + (lane >> 5), piece = lane & 31;
+  const int col = 16 * ((piece >> 1) ^ Tile::swizzle(row0)) + 8 * (piece & 1);
+  unsigned from_d[4], from_x[4];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-#pragma unroll
-    for (int i = 0; i < KT; ++i)
-      *reinterpret_cast<f32x4_t*>(mine + (lane & 15) * kRow + 4 * (16 * i + 4 * (lane >> 4))) = acc[i][j];
-    fence();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = 2 * i + (lane >> 5), row = n0 + 16 * (NT * wn + j) + at;
-      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(mine + at * kRow + 16 * (lane & 31));
-      if (row < p.n)
-        store_sums(p.dw + static_cast<int64_t>(row) * p.k, k0 + 128 * wk + 4 * (lane & 31), p.k, v, p.add != 0);
-    }
-    fence();
+  for (int i = 0; i < 4; ++i) {
+    from_d[i] = 2 * ((row0 + 2 * kPairs[i]) * p.n + min(n0 + col, p.n - 8));
+    from_x[i] = 2 * ((row0 + 2 * kPairs[i]) * p.kcols + min(k0 + col, p.kcols - 8));
   }
+  const int chunks = p.tokens / kTokens * (kTokens / kChunk);
+  const uint8_t* base_d = uniform(reinterpret_cast<const uint8_t*>(p.dy));
+  const uint8_t* base_x = uniform(reinterpret_cast<const uint8_t*>(wide));
+  int copied = 0;                                  // chunks
+  unsigned to = lds_address(lds) + 1024 * pair0;   // in the half of the ring that is filled
+  auto copy = [&](int odd, int i) {                // i = 0..3: x, 4..7: dy
+    if (i < 4)
+      copy16_to_lds(base_x, from_x[i], to + 2 * odd * kChunkBytes + 1024 * kPairs[i]);
+    else
+      copy16_to_lds(base_d, from_d[i - 4], to + (2 * odd + 1) * kChunkBytes + 1024 * kPairs[i - 4]);
+  };
+  auto copied_chunk = [&] {                        // past the last chunk it is read again, into a slot nobody reads
+    if (++copied < chunks) {
+      base_x += static_cast<int64_t>(2 * kChunk) * p.kcols;
+      base_d += static_cast<int64_t>(2 * kChunk) * p.n;
+    }
+  };
+  f32x4_t acc[KT][NT] = {};
+  bf16x8_t fx[KR], fx_last[2][KT - KR], fd[2][NT];
+  int at_x[KT], at_d[NT];                          // in the half of the ring that is read
+#pragma unroll
+  for (int i = 0; i < KT; ++i) {
+    at_x[i] = off_x ^ (32 * i);
+    at_d[i] = off_d ^ (32 * i);
+    opaque(at_x[i]);
+    opaque(at_d[i]);
+  }
+  auto read_d = [&](int odd, int i) {
+    fd[odd][i] = read_columns<B>(lds + (2 * odd + 1) * kChunkBytes, at_d[i], 0, 0);
+  };
+  auto read_x = [&](int odd, int i) {
+    (i < KR ? fx[i] : fx_last[odd][i - KR]) = read_columns<B>(lds + 2 * odd * kChunkBytes, at_x[i], 0, 0);
+  };
+  if (chunks > 0) {
+#pragma unroll
+    for (int c = 0; c < kChunkRing; ++c) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) copy(c & 1, i);
+      copied_chunk();
+      if (c & 1) to ^= kPair;
+    }
+    copies_left<8 * (kChunkRing - 2)>();
+    meet();
+#pragma unroll
+    for (int i = 0; i < NT; ++i) read_d(0, i);
+#pragma unroll
+    for (int i = 0; i < KT; ++i) read_x(0, i);
+    reads_done();
+    meet();
+    auto chunk = [&](auto odd_) {
+      constexpr int odd = odd_;
+      fence();
+      if constexpr (odd) {
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+          at_x[i] ^= kPair;
+          at_d[i] ^= kPair;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          multiply_into(i < KR ? fx[i] : fx_last[odd][i - KR], fd[odd][j], acc[i][j]);
+          fence();
+          if (i == 0)
+            read_d(odd ^ 1, j);
+          else if (i == 1 && j < KT - KR)
+            read_x(odd ^ 1, KR + j);
+          else if (j == 2 && i <= KR)
+            read_x(odd ^ 1, i - 1);
+          if (j == 5) copy(odd, i);
+          fence();
+        }
+      copied_chunk();
+      reads_done();
+      copies_left<8 * (kChunkRing - 2)>();
+      meet();
+      if constexpr (odd) to ^= kPair;
+    };
+    for (int c = 0; c < chunks; c += 2) {
+      chunk(std::integral_constant<int, 0>{});
+      chunk(std::integral_constant<int, 1>{});
+    }
+    copies_left<0>();
+  }
+  const int t0 = chunks * kChunk;
+  if (t0 < p.tokens) {                             // what is left over, widened on its way
+    X x;
+    D d;
+    x.load(thread, p.q, p.scale, t0, p.tokens, k0, p.kcols, p.kscales);
+    d.load(thread, p.dy, t0, p.tokens, n0, p.n);
+    __syncthreads();
+    x.store(thread, lds, t0, p.tokens);
+    d.store(thread, lds + Tile::kBytes, t0, p.tokens, n0, p.n);
+    __syncthreads();
+#pragma unroll 1
+    for (int c = 0; c < kTokens / kChunk; ++c) {
+      bf16x8_t tx[KT], td[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) td[j] = read_columns<B>(lds + Tile::kBytes, off_d, j, c);
+#pragma unroll
+      for (int i = 0; i < KT; ++i) tx[i] = read_columns<B>(lds, off_x, i, c);
+      reads_done();
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) multiply_into(tx[i], td[j], acc[i][j]);
+    }
+  }
+  accumulators_done();
+  __syncthreads();
+  store_wgrad_tile<KT, NT>(p, lds + wave * kStoreBytes, n0 + 16 * NT * wn, k0 + 16 * KT * wk, acc);
 }
 
 // out = (out +) the partial sums, in order; fp32, or rounded once to bf16.
@@ -1135,11 +1346,19 @@ void launch_wgrad_tiles(const WgradArgs& p, hipStream_t stream) {
 }
 
 void launch_wgrad_turns(const WgradArgs& p, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(tiles_of(p.n, p.k, 256, 256)));
-  if (p.n % 8 == 0)
-    hipLaunchKernelGGL(wgrad_turns_kernel<kDyWhole>, grid, dim3(512), 0, stream, p);
-  else
-    hipLaunchKernelGGL(wgrad_turns_kernel<kDyOdd>, grid, dim3(512), 0, stream, p);
+  hipLaunchKernelGGL(wgrad_turns_kernel, dim3(static_cast<unsigned>(tiles_of(p.n, p.k, 256, 256))), dim3(512), 0,
+                     stream, p);
+}
+
+int64_t widened_rows(int64_t tokens) { return tokens / kTokens * kTokens; }
+
+void launch_wgrad_copies(const WgradArgs& p, uint16_t* wide, hipStream_t stream) {
+  const int64_t rows = widened_rows(p.tokens);
+  if (rows > 0)
+    hipLaunchKernelGGL(widen_rows_kernel, dim3(static_cast<unsigned>((rows * (p.kcols / 16) + 255) / 256)), dim3(256), 0,
+                       stream, p.q, p.scale, rows, p.kcols, p.kscales, wide);
+  hipLaunchKernelGGL(wgrad_copies_kernel, dim3(static_cast<unsigned>(tiles_of(p.n, p.k, 256, 256))), dim3(256), 0,
+                     stream, p, wide);
 }
 
 // Which kernel, and over how many runs of tokens whose partial sums go through
@@ -1147,7 +1366,8 @@ void launch_wgrad_turns(const WgradArgs& p, hipStream_t stream) {
 // step of 64 tokens, measured: 64 x 64 tiles 0.37 while there are few
 // workgroups and 0.12 + 1 / 1050 each then (169: 0.37, 650: 0.75, 1024: 1.05,
 // 4096: 3.6); 128 x 128 tiles 0.65 and from 254 on 1 / 390 each (169: 0.63, 256:
-// 0.75, 650: 1.7); 256 x 256 tiles 1.7 a round of 256.  Partial sums cost their
+// 0.75, 650: 1.7); 256 x 256 tiles 1.7 a round of 256, or 1.5 and the widening
+// where rows of dy are aligned.  Partial sums cost their
 // traffic at 4.5 TB/s and a launch.
 struct WgradPlan {
   int tile, splits, split_steps;
@@ -1156,7 +1376,10 @@ WgradPlan wgrad_plan(int64_t tokens, int64_t n, int64_t k) {
   const int64_t steps = (tokens + kTokens - 1) / kTokens;
   const int64_t t64 = tiles_of(n, k, 64, 64), t128 = tiles_of(n, k, 128, 128), t256 = tiles_of(n, k, 256, 256);
   WgradPlan best{256, 1, static_cast<int>(steps)};
-  double least = n >= 8 ? 10 + 1.7 * static_cast<double>(steps) * static_cast<double>((t256 + 255) / 256) : 1e30;
+  const double rounds = static_cast<double>((t256 + 255) / 256);
+  double least = n % 8 == 0 ? 12 + 1.5 * static_cast<double>(steps) * rounds + 0.6e-6 * static_cast<double>(tokens * k)
+               : n >= 8     ? 10 + 1.7 * static_cast<double>(steps) * rounds
+                            : 1e30;
   for (int splits = 1; splits <= 32 && (splits == 1 || splits * 4 <= steps); ++splits) {
     const int64_t each = (steps + splits - 1) / splits;
     if ((steps + each - 1) / each != splits) continue;
@@ -1184,6 +1407,8 @@ void launch_wgrad(const WgradArgs& args, float* workspace, hipStream_t stream) {
     launch_wgrad_tiles<2, 2, 2, 2>(p, stream);
   else if (plan.tile == 128)
     launch_wgrad_tiles<4, 2, 2, 4>(p, stream);
+  else if (p.n % 8 == 0)
+    launch_wgrad_copies(p, reinterpret_cast<uint16_t*>(workspace), stream);
   else
     launch_wgrad_turns(p, stream);
   if (plan.splits > 1)
@@ -1223,8 +1448,9 @@ taco_status_t taco_matmul_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_
 
 size_t taco_wgrad_fp8_workspace_bytes(int64_t tokens, int64_t n, int64_t k) {
   if (!matrix_ok(tokens, n) || !matrix_ok(tokens, k) || !matrix_ok(n, k)) return 0;
-  const int splits = wgrad_plan(tokens, n, k).splits;
-  return splits > 1 ? static_cast<size_t>(4 * n * k) * splits : 0;
+  const WgradPlan plan = wgrad_plan(tokens, n, k);
+  if (plan.tile == 256) return n % 8 == 0 ? static_cast<size_t>(2 * widened_rows(tokens) * fp8_cols(k)) : 0;
+  return plan.splits > 1 ? static_cast<size_t>(4 * n * k) * plan.splits : 0;
 }
 
 taco_status_t taco_wgrad_fp8(const void* dy_bf16, const uint8_t* q, const uint8_t* scale, int64_t tokens, int64_t n,
