@@ -401,45 +401,66 @@ __global__ __launch_bounds__(64 * kFewWaves) void matmul_few_kernel(
   }
 }
 
-// The large product: 256 x 256 tiles, 8 wavefronts of 128 rows of b by 64 of a.
+// One product of 128 columns into accumulators that stay in the accumulation
+// registers, which the compiler would otherwise move to and from the others
+// around each use.  It does not see a matrix instruction here:
+// accumulators_done() has to stand before anything else reads them, and the
+// operands come straight from LDS reads that were waited for.
+__device__ __forceinline__ void multiply_into(const i32x8_t& b, const i32x8_t& a, f32x4_t& acc, int sb, int sa) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+               : "+a"(acc) : "v"(b), "v"(a), "v"(sb), "v"(sa));
+#endif
+}
+
+__device__ __forceinline__ void accumulators_done() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
+// All LDS reads of the wavefront are done, known to the compiler as well.
+__device__ __forceinline__ void reads_done() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0), nothing else
+  __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
+// The large product: 256 x 256 tiles, four wavefronts of 128 x 128 each.
 //
-// Two groups of wavefronts take turns.  A SIMD holds one wavefront of each
-// group; while one group's matrix instructions run, the other reads its next
-// fragments, so neither the LDS latency nor the reads' bandwidth shows.  A step
-// (128 columns) has four phases with a barrier of the whole workgroup after
-// each: M1, read a's fragments and the first half of b's; C1, multiply; M2,
-// read b's second half; C2, multiply.  The second group runs one phase behind.
+// Two steps of 128 columns of each operand lie in LDS.  While a wavefront
+// multiplies step k it reads its fragments of step k + 1 between the matrix
+// instructions: in the first half a's, into a second set of registers, and in the
+// second half b's, into the registers whose eight products are done (the last
+// two into a second set).  So a's part of step k + 1 is free in the middle of
+// step k, and is overwritten with step k + 3's from there on; b's is free at its
+// end, and is overwritten with step k + 3's in the first half of step k + 1.
+// Either copy has one and a half steps to land.  A barrier stands in the
+// middle and at the end of a step; before it each wavefront has done its reads
+// and waits until only the copies of the last two halves (eight each) are in
+// flight.  Operations issued later only make a wait stricter.
 //
-// The operands stream through a ring of nine 16 KiB units in LDS, four per
-// step in the order b's first halves, a's rows 0..127, a's rows 128..255, b's
-// second halves.  Unit u goes to slot u % 9 once unit u - 9 has been read by
-// both groups: with P1..P4 the phases in which the first group is in M1(k),
-// C1(k), M2(k), C2(k) and the second in C2(k - 1), M1(k), C1(k), M2(k), unit
-// 4 k + 8 may be issued from P1 on and units 4 k + 9..11 from P3 on.  Either
-// group issues its copies in its own M1 and M2, where they do not hold up the
-// matrix instructions.  Before the barrier that frees a unit for reading, every
-// wavefront waits until only newer units are in flight: unit 4 k + 3 is due at
-// the end of P2 and unit 4 k + 6 at the end of P4, with five newer ones (ten
-// copies of a wavefront) each.  Copies retire in issue order, so operations
-// issued later only make a wait stricter.
-//
-// 8192 x 8192 x 8192: 375 to 400 us on different cards, 2.75 to 2.9 PFLOP/s;
-// 8192 x 14336 x 3584: 310 to 335 us, 2.5 to 2.7.  A step takes about 1.4 us where
-// its matrix instructions alone take 1.02, a tile's start and end about 4.  When
-// 8192^3 took 383 us it took 324 without the loop's copies, 321 without the LDS
-// reads, and the copies alone 206: the two compete for LDS and the barriers cost
-// the rest.  With one step in flight (two whole buffers) it took 435 us, with the
-// copies among the matrix instructions 390.
+// 8192 x 8192 x 8192: 365 us, 3.0 PFLOP/s; 8192 x 14336 x 3584: 313 us, 2.7 (on
+// the same card 392 and 331 with eight wavefronts of 64 x 128 that take turns
+// and a third more LDS reads).  Of the 365, 285 are the matrix instructions at
+// the clock they run at; the copies add 63 to them and the reads 15 to 18.  The copies'
+// cost is not their latency (waiting for fewer of them changes nothing), and
+// spreading them over the half steps does not lower it.  A tile's start and
+// end take about 8 us, so at k = 512 the kernel is a tenth slower than that one.
 constexpr int kBig = 256;                       // rows of either operand in a tile
-constexpr int kUnit = 128 * kBlock;             // bytes: 128 rows of 128 columns
-constexpr int kRing = 9;
+constexpr int kOperand = kBig * kBlock;         // bytes of a step
 constexpr int kScaleBuffer = 2048;              // a dword of scale bytes (four steps) for each row, twice over
 
-__global__ __launch_bounds__(512) void matmul_turns_kernel(
+__global__ __launch_bounds__(256) void matmul_large_kernel(
     const uint8_t* __restrict__ qa, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ qb,
     const uint8_t* __restrict__ sb, int m, int n, int kcols, int kscales, uint16_t* __restrict__ y) {
-  constexpr int NT = 8, MT = 4;
-  __shared__ __align__(128) uint8_t lds[kRing * kUnit + 2 * kScaleBuffer];
+  constexpr int NT = 8, MT = 8;
+  constexpr int NR = NT - 2;                       // b fragments read into the registers they were in
+  __shared__ __align__(128) uint8_t lds[4 * kOperand + 2 * kScaleBuffer];      // a, a, b, b, scales
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles_m = (m + kBig - 1) / kBig, tiles_n = (n + kBig - 1) / kBig;
@@ -449,118 +470,120 @@ __global__ __launch_bounds__(512) void matmul_turns_kernel(
   const int r = lane & 15, g = lane >> 4;
   const int wn = wave & 1, wm = wave >> 1;
 
-  // Copies: a wavefront fills rows 16 wave + 0..15 of every unit.  Rows past
-  // the end are read from the last row; what they give is never stored.
+  // Copies: a wavefront fills 64 rows of either operand, eight at a time.  Rows
+  // past the end are read from the last row; what they give is never stored.
   const uint8_t* gb = uniform(qb + static_cast<int64_t>(n0) * kcols);
   const uint8_t* ga = uniform(qa + static_cast<int64_t>(m0) * kcols);
   const int left_n = n - 1 - n0, left_m = m - 1 - m0;
-  unsigned off_b1[2], off_b2[2], off_a1[2], off_a2[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = 16 * wave + 8 * i + (lane >> 3), row_b = (row & 64) + row;     // b: 64 rows of each half tile
-    const unsigned chunk = 16 * ((lane & 7) ^ (lane >> 3));
-    off_b1[i] = static_cast<unsigned>(min(row_b, left_n)) * kcols + chunk;
-    off_b2[i] = static_cast<unsigned>(min(row_b + 64, left_n)) * kcols + chunk;
-    off_a1[i] = static_cast<unsigned>(min(row, left_m)) * kcols + chunk;
-    off_a2[i] = static_cast<unsigned>(min(row + 128, left_m)) * kcols + chunk;
-  }
-  // Scale bytes: wavefronts 0..3 take a dword of 64 rows of a each, the others
-  // (all alike) the dwords of b's two blocks.
-  const uint8_t* gs = uniform(wave < 4 ? sa + static_cast<int64_t>(m0) * kscales
-                                       : sb + static_cast<int64_t>(n0 / kBlock) * kscales);
-  const unsigned off_s = (wave < 4 ? static_cast<unsigned>(min(64 * wave + lane, left_m))
-                                   : static_cast<unsigned>(min(lane & 1, left_n / kBlock))) * kscales;
-  const unsigned lds0 = lds_address(lds) + 2048 * wave;
-  const unsigned lds_s = lds_address(lds) + kRing * kUnit + 256 * wave;
-  auto copy_unit = [&](const uint8_t* base, const unsigned (&off)[2], int k, int slot) {
-    copy16_to_lds(base + k * kBlock, off[0], lds0 + slot * kUnit);
-    copy16_to_lds(base + k * kBlock, off[1], lds0 + slot * kUnit + 1024);
+  const unsigned chunk = 16 * ((lane & 7) ^ (lane >> 3)), first = (64 * wave + (lane >> 3)) * kcols + chunk;
+  const unsigned last_a = static_cast<unsigned>(left_m) * kcols + chunk;
+  const unsigned last_b = static_cast<unsigned>(left_n) * kcols + chunk;
+  const int steps = kcols / kBlock;
+  const unsigned lds0 = lds_address(lds) + 64 * kBlock * wave;
+  auto copy_a = [&](int k, int odd, int i) {
+    copy16_to_lds(ga + min(k, steps - 1) * kBlock, min(first + 8 * i * kcols, last_a), lds0 + odd * kOperand + 1024 * i);
   };
-  auto copy_scales = [&](int k) { copy4_to_lds(gs + k, off_s, lds_s + (k >> 2 & 1) * kScaleBuffer); };
-  auto slot_after = [](int slot, int d) { return slot + d >= kRing ? slot + d - kRing : slot + d; };
+  auto copy_b = [&](int k, int odd, int i) {
+    copy16_to_lds(gb + min(k, steps - 1) * kBlock, min(first + 8 * i * kcols, last_b),
+                  lds0 + (2 + odd) * kOperand + 1024 * i);
+  };
+  // Scale bytes: a dword of 64 rows of a, and (all wavefronts alike) of b's two blocks.
+  const uint8_t* gsa = uniform(sa + static_cast<int64_t>(m0) * kscales);
+  const uint8_t* gsb = uniform(sb + static_cast<int64_t>(n0 / kBlock) * kscales);
+  const unsigned from_sa = static_cast<unsigned>(min(64 * wave + lane, left_m)) * kscales;
+  const unsigned from_sb = static_cast<unsigned>(min(lane & 1, left_n / kBlock)) * kscales;
+  const unsigned lds_s = lds_address(lds) + 4 * kOperand + 256 * wave;
+  auto copy_scales = [&](int k) {
+    copy4_to_lds(gsa + k, from_sa, lds_s + (k >> 2 & 1) * kScaleBuffer);
+    copy4_to_lds(gsb + k, from_sb, lds_s + (k >> 2 & 1) * kScaleBuffer + 1024);
+  };
 
   const int lane_off = r * kBlock + 16 * (g ^ (r & 7));
+  int at_a = 128 * kBlock * wm + lane_off, at_b = 2 * kOperand + 128 * kBlock * wn + lane_off;
+  opaque(at_a);
+  opaque(at_b);
   f32x4_t acc[NT][MT] = {};
-  const int steps = kcols / kBlock;
+  i32x8_t fa[2][MT], fb[NR], fb_last[2][NT - NR];
+  int scale_a[2][MT], scale_b[2];
+  auto read_a = [&](int odd, int j) { fa[odd][j] = load_fragment(lds + odd * kOperand + 16 * kBlock * j, at_a); };
+  auto read_b = [&](int odd, int i) {
+    (i < NR ? fb[i] : fb_last[odd][i - NR]) = load_fragment(lds + odd * kOperand + 16 * kBlock * i, at_b);
+  };
+  const int at_s = 4 * kOperand + 4 * (128 * wm + r);
+  auto read_scale = [&](int k, int odd, int j) {   // j = MT: b's
+    const uint8_t* s = lds + (k >> 2 & 1) * kScaleBuffer + (k & 3);
+    if (j < MT) scale_a[odd][j] = s[at_s + 64 * j];
+    else scale_b[odd] = s[4 * kOperand + 1024 + 4 * wn];
+  };
   copy_scales(0);
-  copy_unit(gb, off_b1, 0, 0);
-  copy_unit(ga, off_a1, 0, 1);
-  copy_unit(ga, off_a2, 0, 2);
-  copy_unit(gb, off_b2, 0, 3);
-  if (steps > 1) {
-    copy_unit(gb, off_b1, 1, 4);
-    copy_unit(ga, off_a1, 1, 5);
-    copy_unit(ga, off_a2, 1, 6);
-    copy_unit(gb, off_b2, 1, 7);
-    copies_left<10>();
-  } else {
-    copies_left<2>();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) copy_a(k, k, i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) copy_b(k, k, i);
   }
+  copies_left<16>();
+  meet();
+#pragma unroll
+  for (int j = 0; j < MT; ++j) read_a(0, j);
+#pragma unroll
+  for (int i = 0; i < NT; ++i) read_b(0, i);
+#pragma unroll
+  for (int j = 0; j <= MT; ++j) read_scale(0, 0, j);
+  reads_done();
+  meet();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) copy_a(2, 0, i);
+  copies_left<16>();
   meet();
 
-  auto run = [&](auto group) {
-    constexpr bool kSecond = group.value;
-    int slot = 0;                                  // of the step's first unit
-    if constexpr (kSecond) meet();
-    // TAIL 0: steps that have two more after them, 1: the last but one, 2: the last.
-    auto step = [&](int k, auto tail) {
-      constexpr int TAIL = tail.value;
-      const uint8_t* scales = lds + kRing * kUnit + (k >> 2 & 1) * kScaleBuffer + (k & 3);
-      const uint8_t* tb = lds + slot * kUnit + 64 * kBlock * wn;
-      const uint8_t* ta = lds + slot_after(slot, wm < 2 ? 1 : 2) * kUnit + 64 * kBlock * (wm & 1);
-      const uint8_t* tb2 = lds + slot_after(slot, 3) * kUnit + 64 * kBlock * wn;
-      auto m1_copies = [&] {
-        if constexpr (TAIL == 0) {
-          if ((k & 3) == 0 && k + 4 < steps) copy_scales(k + 4);
-          copy_unit(gb, off_b1, k + 2, slot_after(slot, 8));
+  auto step = [&](int k, auto odd_) {
+    constexpr int odd = odd_;
+    fence();
+    if ((k & 3) == 0 && k + 4 < steps) copy_scales(k + 4);
+    const int next = min(k + 1, steps - 1);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        const int at = i * MT + j;
+        if (at == 32) {
+          reads_done();
+          copies_left<16>();
+          meet();
         }
-      };
-      auto m2_copies = [&] {
-        if constexpr (TAIL == 0) {
-          copy_unit(ga, off_a1, k + 2, slot);
-          copy_unit(ga, off_a2, k + 2, slot_after(slot, 1));
-          copy_unit(gb, off_b2, k + 2, slot_after(slot, 2));
+        multiply_into(i < NR ? fb[i] : fb_last[odd][i - NR], fa[odd][j], acc[i][j], scale_b[odd], scale_a[odd][j]);
+        fence();
+        if (at < 16) {
+          if (at % 2 == 0) copy_b(k + 2, odd, at / 2);
+          else read_a(odd ^ 1, at / 2);
+        } else if (at <= 16 + MT) {
+          read_scale(next, odd ^ 1, at - 16);
+        } else if (at >= 32 && at < 48) {
+          if (at % 2 == 0) copy_a(k + 3, odd ^ 1, (at - 32) / 2);
+          else if (at < 40) read_b(odd ^ 1, (at - 33) / 2);
+          else if (at < 44) read_b(odd ^ 1, NR + (at - 41) / 2);
+          else if (at == 45) read_b(odd ^ 1, 4);
+        } else if (at == 49) {
+          read_b(odd ^ 1, 5);
         }
-      };
-      auto p2_wait = [&] { copies_left<TAIL == 0 ? 10 : TAIL == 1 ? 8 : 0>(); };   // this step's last unit
-      auto p4_wait = [&] { copies_left<TAIL == 0 ? 10 : TAIL == 1 ? 2 : 0>(); };   // the next step's first three
-      i32x8_t a[MT], b[NT / 2];
-      int scale_a[MT];
-#pragma unroll
-      for (int i = 0; i < NT / 2; ++i) b[i] = load_fragment(tb + 16 * kBlock * i, lane_off);
-#pragma unroll
-      for (int j = 0; j < MT; ++j) a[j] = load_fragment(ta + 16 * kBlock * j, lane_off);
-#pragma unroll
-      for (int j = 0; j < MT; ++j) scale_a[j] = scales[4 * (64 * wm + 16 * j + r)];
-      const int scale_b = scales[1024 + 4 * wn];
-      m1_copies();
-      if constexpr (kSecond) p2_wait();
-      reads_done_and_meet();
-      multiply(b, a, scale_b, scale_a, &acc[0][0]);
-      if constexpr (!kSecond) p2_wait();
-      meet();
-#pragma unroll
-      for (int i = 0; i < NT / 2; ++i) b[i] = load_fragment(tb2 + 16 * kBlock * i, lane_off);
-      m2_copies();
-      if constexpr (kSecond) p4_wait();
-      reads_done_and_meet();
-      multiply(b, a, scale_b, scale_a, &acc[NT / 2][0]);
-      if constexpr (!kSecond) p4_wait();
-      meet();
-      slot = slot_after(slot, 4);
-    };
-    int k = 0;
-    for (; k + 2 < steps; ++k) step(k, std::integral_constant<int, 0>{});
-    if (steps > 1) step(steps - 2, std::integral_constant<int, 1>{});
-    step(steps - 1, std::integral_constant<int, 2>{});
-    if constexpr (!kSecond) meet();
+        fence();
+      }
+    reads_done();
+    copies_left<16>();
+    meet();
   };
-  if (wave >= 4)
-    run(std::true_type{});
-  else
-    run(std::false_type{});
-  // A wavefront's 64 x 128 results go through LDS, so that a store covers four
-  // whole rows of 256 bytes and not 16 pieces of 32.
+  int k = 0;
+  for (; k + 1 < steps; k += 2) {
+    step(k, std::integral_constant<int, 0>{});
+    step(k + 1, std::integral_constant<int, 1>{});
+  }
+  if (k < steps) step(k, std::integral_constant<int, 0>{});
+  copies_left<0>();
+  accumulators_done();
+  // 64 x 128 results of a wavefront at a time go through LDS, so that a store
+  // covers four whole rows of 256 bytes and not 16 pieces of 32.
   constexpr int kRow = 256 + 16;                   // bytes, apart by a bank group
   __syncthreads();
   int thread = threadIdx.x;
@@ -568,17 +591,23 @@ __global__ __launch_bounds__(512) void matmul_turns_kernel(
   const int er = thread & 15, eg = thread >> 4 & 3;
   uint8_t* mine = lds + wave * (64 * kRow);
 #pragma unroll
-  for (int j = 0; j < MT; ++j)
+  for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-      *reinterpret_cast<uint2*>(mine + (16 * j + er) * kRow + 2 * (16 * i + 4 * eg)) =
-          make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
-  fence();
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int row = m0 + 64 * wm + 4 * i + eg;
-    const uint4 v = *reinterpret_cast<const uint4*>(mine + (4 * i + eg) * kRow + 16 * er);
-    if (row < m) store_chunk<false>(y + static_cast<int64_t>(row) * n, n0 + 128 * wn + 8 * er, n, v);
+      for (int i = 0; i < NT; ++i) {
+        const f32x4_t v = acc[i][4 * h + j];
+        *reinterpret_cast<uint2*>(mine + (16 * j + er) * kRow + 2 * (16 * i + 4 * eg)) =
+            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+      }
+    fence();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int row = m0 + 128 * wm + 64 * h + 4 * i + eg;
+      const uint4 v = *reinterpret_cast<const uint4*>(mine + (4 * i + eg) * kRow + 16 * er);
+      if (row < m) store_chunk<false>(y + static_cast<int64_t>(row) * n, n0 + 128 * wn + 8 * er, n, v);
+    }
+    fence();
   }
 }
 
@@ -893,9 +922,9 @@ __device__ __forceinline__ void store_wgrad_tile(const WgradArgs& p, uint8_t* mi
 }
 
 // The large gradient where dy's rows start anywhere (n no multiple of 8), so that
-// they pass through registers: 256 x 256 tiles, two groups of four wavefronts that take
-// turns as in matmul_turns_kernel: while one group multiplies 32 rows of t, the
-// other reads its fragments of 32.  A step of 64 rows has four phases, M0, C0,
+// they pass through registers: 256 x 256 tiles, two groups of four wavefronts,
+// one of each on a SIMD, that take turns: while one group multiplies 32 rows of
+// t, the other reads its fragments of 32.  A step of 64 rows has four phases, M0, C0,
 // M1, C1, the second group one behind.  The thread's part of step s + 1 goes
 // from registers to LDS in C0 of step s, between the matrix instructions, when
 // both groups are done with step s - 1 in that buffer; both have waited for
@@ -1011,31 +1040,10 @@ __global__ __launch_bounds__(512) void wgrad_turns_kernel(const WgradArgs p) {
   store_wgrad_tile<KT, NT>(p, lds + wave * kStoreBytes, n0 + 16 * NT * wn, k0 + 16 * KT * wk, acc);
 }
 
-// One product into accumulators that stay in the accumulation registers, which
-// the compiler would otherwise move to and from the others around each use.  It
-// does not see a matrix instruction here: accumulators_done() has to stand
-// before anything else reads them, and the operands come straight from LDS reads
-// that were waited for.
+// One product of 32 rows of t, as in the FP8 product.
 __device__ __forceinline__ void multiply_into(const bf16x8_t& x, const bf16x8_t& d, f32x4_t& acc) {
 #if defined(__HIP_DEVICE_COMPILE__)
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(x), "v"(d));
-#endif
-}
-
-__device__ __forceinline__ void accumulators_done() {
-#if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-#endif
-}
-
-// All LDS reads of the wavefront are done, known to the compiler as well.
-__device__ __forceinline__ void reads_done() {
-#if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0), nothing else
-  __builtin_amdgcn_sched_barrier(0);
 #endif
 }
 
@@ -1291,26 +1299,26 @@ Splits matmul_splits(int64_t m, int64_t n, int64_t kcols) {
 }
 
 void launch_big(const MatmulArgs& p, hipStream_t stream) {
-  hipLaunchKernelGGL(matmul_turns_kernel, dim3(static_cast<unsigned>(tiles_of(p.m, p.n, kBig, kBig))), dim3(512), 0,
+  hipLaunchKernelGGL(matmul_large_kernel, dim3(static_cast<unsigned>(tiles_of(p.m, p.n, kBig, kBig))), dim3(256), 0,
                      stream, p.qa, p.sa, p.qb, p.sb, p.m, p.n, p.kcols, p.kscales, p.y);
 }
 
 // Which kernel: by the number of tiles against the 256 CUs.  Measured (us):
 //   m     n     k      64x64 KG 2  64x64 KG 1  128x128 KG 2  128x128 KG 1  256x256
-//   256   4096  4096   10.8        13.4        20.4          24.6          39.1
-//   777   1601  1600   11.3        8.6         10.9          12.4          20.3
-//   512   4096  4096   20.0        16.8        20.6          24.8          39.5
-//   1024  4096  4096   38.4        30.5        21.7          25.5          40.1
-//   2048  4096  4096   75.7        54.4        41.5          33.3          41.6
-//   2816  4096  4096                                         56.6          44.2
-//   4096  4096  4096   153         111         105           75.7          55.1
-//   4608  4096  4096                           106           89.7          87.4
-//   8192  4224  512                            44.9          30.5          33.9
-//   8192  3584  1000   99.4        56.6        50.0          39.2          33.6
+//   256   4096  4096   10.8        13.4        20.4          24.6          36.6
+//   777   1601  1600   11.3        8.6         10.9          12.4          21.3
+//   512   4096  4096   20.0        16.8        20.6          24.9          36.8
+//   1024  4096  4096   38.4        30.5        21.7          25.4          37.5
+//   2048  4096  4096   75.7        54.4        41.5          31.7          38.7
+//   2816  4096  4096                                         52.7          40.1
+//   4096  4096  4096   153         111         105           74.5          51.4
+//   4608  4096  4096                           106           87.9          82.5
+//   8192  4224  512                            44.9          29.5          37.0
+//   8192  3584  1000   99.4        56.6        50.0          37.6          33.1
 // so 64 x 64 tiles until a CU would have more than three, two groups of
 // wavefronts for a tile where a CU has one; 128 x 128 while their workgroups
 // are all resident (two to a CU), and 256 x 256 from there on, which loses up to
-// a tenth where few columns meet a nearly empty last round.
+// a quarter where few columns meet a nearly empty last round.
 // Up to 32 rows the direct loads win (16 rows: 6.7 against 9.7, 32: 9.5 against
 // 10.1), and at 64 rows the tiles do (15.2 against 10.5).
 void launch_matmul(const MatmulArgs& p, hipStream_t stream) {
@@ -1366,8 +1374,9 @@ void launch_wgrad_copies(const WgradArgs& p, uint16_t* wide, hipStream_t stream)
 // step of 64 tokens, measured: 64 x 64 tiles 0.37 while there are few
 // workgroups and 0.12 + 1 / 1050 each then (169: 0.37, 650: 0.75, 1024: 1.05,
 // 4096: 3.6); 128 x 128 tiles 0.65 and from 254 on 1 / 390 each (169: 0.63, 256:
-// 0.75, 650: 1.7); 256 x 256 tiles 1.7 a round of 256, or 1.5 and the widening
-// where rows of dy are aligned.  Partial sums cost their
+// 0.75, 650: 1.7); 256 x 256 tiles 1.7 a round of 256, or 1.45 and the widening
+// where rows of dy are aligned, and 8 for a round's stores, which nothing
+// overlaps (256 x 8192 x 8192: 79 against 70 with 128 x 128).  Partial sums cost their
 // traffic at 4.5 TB/s and a launch.
 struct WgradPlan {
   int tile, splits, split_steps;
@@ -1377,8 +1386,8 @@ WgradPlan wgrad_plan(int64_t tokens, int64_t n, int64_t k) {
   const int64_t t64 = tiles_of(n, k, 64, 64), t128 = tiles_of(n, k, 128, 128), t256 = tiles_of(n, k, 256, 256);
   WgradPlan best{256, 1, static_cast<int>(steps)};
   const double rounds = static_cast<double>((t256 + 255) / 256);
-  double least = n % 8 == 0 ? 12 + 1.5 * static_cast<double>(steps) * rounds + 0.6e-6 * static_cast<double>(tokens * k)
-               : n >= 8     ? 10 + 1.7 * static_cast<double>(steps) * rounds
+  double least = n % 8 == 0 ? 4 + (8 + 1.45 * static_cast<double>(steps)) * rounds + 0.6e-6 * static_cast<double>(tokens * k)
+               : n >= 8     ? 4 + (8 + 1.7 * static_cast<double>(steps)) * rounds
                             : 1e30;
   for (int splits = 1; splits <= 32 && (splits == 1 || splits * 4 <= steps); ++splits) {
     const int64_t each = (steps + splits - 1) / splits;

@@ -23,7 +23,7 @@ def operands(t, n, k):
 
 # 16-byte aligned rows of dy and others; fewer rows than a step, one step, and rows left over
 @pytest.mark.parametrize("n,k", [(16000, 16100), (15999, 16100)])
-@pytest.mark.parametrize("t", [1, 40, 63, 64, 65, 100, 128, 192, 230, 256, 453])
+@pytest.mark.parametrize("t", [1, 40, 63, 64, 65, 100, 128, 192, 230, 256, 453, 512, 575, 640, 705, 768, 961])
 def test_wgrad_exact_sums(t, n, k):
     dy, q, scale, x = operands(t, n, k)
     want = dy.float().t().contiguous() @ x
@@ -36,7 +36,7 @@ def test_wgrad_exact_sums(t, n, k):
     assert (whole[:2048] == 7).all() and (whole[2048 + n * k:] == 7).all()
 
 
-@pytest.mark.parametrize("t,row", [(100, 99), (100, 5), (128, 127), (30, 29)])
+@pytest.mark.parametrize("t,row", [(100, 99), (100, 5), (128, 127), (30, 29), (800, 799), (800, 5)])
 @pytest.mark.parametrize("n,k", [(16000, 16100), (15999, 16100)])
 def test_wgrad_non_finite_stays_in_its_line(t, row, n, k):
     dy, q, scale, x = operands(t, n, k)
