@@ -1047,7 +1047,8 @@ __device__ __forceinline__ void multiply_into(const bf16x8_t& x, const bf16x8_t&
 #endif
 }
 
-// The quantised rows widened to bf16, 16 codes per thread: 4096 x 4096 in 9 us.
+// The quantised rows widened to bf16, 16 codes per thread: 4096 x 4096 in 13 us, 3.9
+// TB/s, mostly its writes.
 __global__ __launch_bounds__(256) void widen_rows_kernel(const uint8_t* __restrict__ q,
                                                          const uint8_t* __restrict__ scale, int64_t rows, int kcols,
                                                          int kscales, uint16_t* __restrict__ out) {

@@ -125,7 +125,9 @@ taco_status_t taco_matmul_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_
  *   q, scale  x [tokens, k] in the block format (the layer's quantised input)
  *   dw        out: fp32 [n, k]; read first when accumulate is 1
  * The codes are widened to bf16 on their way into the matrix cores, which is
- * exact because the scales are powers of two (values below 2^-126 excepted).
+ * exact because the scales are powers of two (values below 2^-126 excepted).  The
+ * workspace holds partial sums where tokens are split over workgroups, or the
+ * widened x for large products; it may be NULL where 0 bytes are needed.
  * dy, x and dw within the limits above (TACO_ERR_SHAPE).
  */
 size_t taco_wgrad_fp8_workspace_bytes(int64_t tokens, int64_t n, int64_t k);
