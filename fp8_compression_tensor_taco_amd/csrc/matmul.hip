@@ -413,11 +413,15 @@ __device__ __forceinline__ void multiply_into(const i32x8_t& b, const i32x8_t& a
 #endif
 }
 
-__device__ __forceinline__ void accumulators_done() {
+// The wait passes every accumulator through, so that nothing can read one before it.
+template <int N>
+__device__ __forceinline__ void accumulators_done(f32x4_t (&acc)[N][8]) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    asm volatile("s_nop 15\n\ts_nop 15"
+                 : "+a"(acc[i][0]), "+a"(acc[i][1]), "+a"(acc[i][2]), "+a"(acc[i][3]), "+a"(acc[i][4]),
+                   "+a"(acc[i][5]), "+a"(acc[i][6]), "+a"(acc[i][7]));
 #endif
 }
 
@@ -581,7 +585,7 @@ __global__ __launch_bounds__(256) void matmul_large_kernel(
   }
   if (k < steps) step(k, std::integral_constant<int, 0>{});
   copies_left<0>();
-  accumulators_done();
+  accumulators_done(acc);
   // 64 x 128 results of a wavefront at a time go through LDS, so that a store
   // covers four whole rows of 256 bytes and not 16 pieces of 32.
   constexpr int kRow = 256 + 16;                   // bytes, apart by a bank group
@@ -1218,7 +1222,7 @@ __global__ __launch_bounds__(256) void wgrad_copies_kernel(const WgradArgs p, co
         for (int j = 0; j < NT; ++j) multiply_into(tx[i], td[j], acc[i][j]);
     }
   }
-  accumulators_done();
+  accumulators_done(acc);
   __syncthreads();
   store_wgrad_tile<KT, NT>(p, lds + wave * kStoreBytes, n0 + 16 * NT * wn, k0 + 16 * KT * wk, acc);
 }
