@@ -476,12 +476,13 @@ __global__ __launch_bounds__(256) void matmul_large_kernel(
 
   // Copies: a wavefront fills 64 rows of either operand, eight at a time.  Rows
   // past the end are read from the last row; what they give is never stored.
+  // The last row is the tile's, so that its offset stays inside 32 bits.
   const uint8_t* gb = uniform(qb + static_cast<int64_t>(n0) * kcols);
   const uint8_t* ga = uniform(qa + static_cast<int64_t>(m0) * kcols);
   const int left_n = n - 1 - n0, left_m = m - 1 - m0;
   const unsigned chunk = 16 * ((lane & 7) ^ (lane >> 3)), first = (64 * wave + (lane >> 3)) * kcols + chunk;
-  const unsigned last_a = static_cast<unsigned>(left_m) * kcols + chunk;
-  const unsigned last_b = static_cast<unsigned>(left_n) * kcols + chunk;
+  const unsigned last_a = static_cast<unsigned>(min(left_m, kBig - 1)) * kcols + chunk;
+  const unsigned last_b = static_cast<unsigned>(min(left_n, kBig - 1)) * kcols + chunk;
   const int steps = kcols / kBlock;
   const unsigned lds0 = lds_address(lds) + 64 * kBlock * wave;
   auto copy_a = [&](int k, int odd, int i) {
