@@ -145,7 +145,7 @@ std::tuple<Tensor, Tensor, Tensor, Tensor> rmsnorm_quantize(const Tensor& x_, co
   check(taco_rmsnorm_quantize(x.data_ptr(), residual.defined() ? residual.data_ptr() : nullptr, weight.data_ptr(),
                               tokens, hidden, static_cast<float>(eps), z.defined() ? z.data_ptr() : nullptr,
                               floats_of(rstd), bytes_of(q), bytes_of(scale), stream_of(stream)));
-  return {z.defined() ? z : x, rstd, q, scale};
+  return {z.defined() ? z : x_, rstd, q, scale};      // x itself, also where the kernel took a copy
 }
 
 std::tuple<Tensor, Tensor> rmsnorm_backward(const Tensor& dy_, const Tensor& z_, const Tensor& rstd_,
