@@ -8,6 +8,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -45,13 +46,25 @@ def compile_flags() -> list[str]:
     ]
 
 
-def build_library(verbose: bool = True) -> str:
-    """Compile every HIP source into ``libtaco.so`` next to this file, and the binding; returns the library's path."""
+def build_library(verbose: bool = True, binding_required: bool = False) -> str:
+    """Compile every HIP source into ``libtaco.so`` next to this file, and the binding; returns the library's path.
+
+    The binding needs a host compiler and the headers of Python and torch, which
+    the library and the compression calls do without.  Where it cannot be built a
+    warning says why, and an older one, which may not fit the new library, is
+    removed; with ``binding_required`` the error is raised."""
     tmp = LIB_PATH + ".tmp"
     cmd = [hipcc(), *compile_flags(), "-shared", "-parallel-jobs=3", *SOURCES, *LINEAR_SOURCES, "-o", tmp]
     _run(cmd, verbose)
     os.replace(tmp, LIB_PATH)
-    build_binding(verbose)
+    try:
+        build_binding(verbose)
+    except (ImportError, OSError, RuntimeError) as e:
+        if os.path.exists(BINDING_PATH):
+            os.remove(BINDING_PATH)
+        if binding_required:
+            raise
+        warnings.warn(f"the binding of the 8-bit linear layer was not built ({e}); the compression calls work without it")
     return LIB_PATH
 
 
