@@ -13,10 +13,12 @@ Codes and scales are uint8 tensors.  ``q.view(torch.float8_e4m3fn)`` and
 from __future__ import annotations
 
 import ctypes
+import os
 
 import torch
 
 from ._binding import _on, load
+from .build import BINDING_PATH
 
 BLOCK = 128
 
@@ -73,8 +75,10 @@ def _binding():
         try:
             from . import _linear_binding
         except ImportError as e:
-            raise ImportError("the binding of the 8-bit linear layer is not built: build it first with "
-                              "`python -m fp8_compression_tensor_taco_amd.build` (no CPU fallback exists)") from e
+            what = ("does not load, it may be of another Python or torch" if os.path.exists(BINDING_PATH)
+                    else "is not built")
+            raise ImportError(f"the binding of the 8-bit linear layer {what}: build it with `python -m "
+                              f"fp8_compression_tensor_taco_amd.build` (no CPU fallback exists); {e}") from e
         _native = _linear_binding
     return _native
 
