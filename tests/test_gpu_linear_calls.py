@@ -16,3 +16,169 @@ def test_norm_without_a_residual_returns_x_itself():
         assert z is x
         for a, b in zip((rstd, q, scale), taco.rmsnorm_quantize(x.contiguous().clone(), weight)[1:]):
             assert torch.equal(a, b)
+
+
+def activations(rows, cols, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(rows, cols, device="cuda", generator=gen) * 0.1).to(torch.bfloat16)
+
+
+def layer(t, n, k, seed=0):
+    """Operands of a layer's calls: (x, dy, quantised x, quantised weight, its transpose)."""
+    x, w, dy = activations(t, k, seed), activations(n, k, seed + 1), activations(t, n, seed + 2)
+    wq, ws, wqt, wst = taco.quantize_weight(w)
+    return x, dy, taco.quantize_rows(x), (wq, ws), (wqt, wst)
+
+
+# ------------------------------------------------------------------ workspaces
+
+def workspace_calls():
+    """(bytes needed, call with a workspace) of each operator that takes one, by the kernel that uses it."""
+    x, dy, xq, w, _ = layer(300, 512, 8192)
+    yield "split product", taco.matmul_fp8_workspace_bytes(300, 512, 8192), \
+        lambda ws: taco.matmul_fp8(*xq, *w, workspace=ws)
+    x2, dy2, xq2, _, _ = layer(2000, 200, 300)
+    yield "split weight gradient", taco.wgrad_fp8_workspace_bytes(2000, 200, 300), \
+        lambda ws: taco.wgrad_fp8(dy2, *xq2, 300, workspace=ws)
+    x3, dy3, xq3, _, _ = layer(700, 4096, 4090)
+    yield "widened rows", taco.wgrad_fp8_workspace_bytes(700, 4096, 4090), \
+        lambda ws: taco.wgrad_fp8(dy3, *xq3, 4090, workspace=ws)
+    for rows, cols in ((300, 1600), (70, 20000)):
+        z, g = activations(rows, cols, 7), activations(rows, cols, 8)
+        rstd = torch.rsqrt(z.float().square().mean(1) + 1e-5)
+        yield f"norm gradient {cols}", taco.rmsnorm_backward_workspace_bytes(rows, cols), \
+            lambda ws, z=z, g=g, rstd=rstd: torch.cat([v.float().flatten() for v in
+                                                       taco.rmsnorm_backward(g, z, rstd, z[0], workspace=ws)])
+
+
+def test_a_workspace_of_the_callers():
+    """Any contents, exactly the bytes that are named, and nothing beside them."""
+    for name, need, call in workspace_calls():
+        assert need > 0, name
+        want = call(None)
+        whole = torch.full((need + 1024,), 0xFF, dtype=torch.uint8, device="cuda")      # NaN in every format
+        for workspace in (whole[512:512 + need], whole[256:]):
+            whole.fill_(0xFF)
+            assert torch.equal(call(workspace), want), name
+            assert (whole[:256] == 0xFF).all() and (whole[512 + need:] == 0xFF).all(), name
+        for bad in (whole[512:511 + need], whole[513:513 + need]):
+            with pytest.raises(taco.TacoError):
+                call(bad)
+        with pytest.raises(ValueError):
+            call(torch.zeros(2 * need, dtype=torch.uint8, device="cuda")[::2])
+        with pytest.raises(ValueError):
+            call(torch.zeros(need, dtype=torch.uint8))
+
+
+def test_a_workspace_may_not_overlap():
+    _, _, xq, w, _ = layer(300, 512, 8192)
+    need = taco.matmul_fp8_workspace_bytes(300, 512, 8192)
+    whole = torch.zeros(need + 300 * 512 * 2, dtype=torch.uint8, device="cuda")
+    with pytest.raises(taco.TacoError) as e:
+        taco.matmul_fp8(*xq, *w, out=whole[:300 * 512 * 2].view(torch.bfloat16).view(300, 512), workspace=whole)
+    assert e.value.name == "TACO_ERR_ALIAS"
+
+
+# ---------------------------------------------------------- layouts and streams
+
+def strided(t):
+    """The same values in a view that is not contiguous, and in one that is misaligned."""
+    wide = torch.zeros(*t.shape[:-1], 2 * t.shape[-1], dtype=t.dtype, device="cuda")
+    every_other = wide[..., ::2]
+    every_other.copy_(t)
+    flat = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")
+    off = flat[1:].view(t.shape)
+    off.copy_(t)
+    return every_other, off
+
+
+def calls(t, n, k):
+    """Every operator as (call, its tensor arguments)."""
+    x, dy, (xq, xs), (wq, ws), (wqt, wst) = layer(t, n, k)
+    r, w = activations(t, k, 5), activations(1, k, 6)[0]
+    z, rstd, _, _ = taco.rmsnorm_quantize(x, w, residual=r)
+    dz, gu, dh = activations(t, k, 9), activations(t, 2 * n, 10), activations(t, n, 11)
+    _, _, cq, cs = taco.swiglu_quantize(gu)
+    return [
+        (lambda a, **kw: taco.quantize_rows(a, **kw), [x]),
+        (lambda a, **kw: taco.quantize_weight(a, **kw), [x]),
+        (lambda a, b, c, **kw: taco.rmsnorm_quantize(a, b, residual=c, **kw), [x, w, r]),
+        (lambda a, b, **kw: taco.rmsnorm_quantize(a, b, **kw), [x, w]),
+        (lambda a, b, c, d, e, **kw: taco.rmsnorm_backward(a, b, c, d, dz=e, **kw), [r, z, rstd, w, dz]),
+        (lambda a, b, c, d, **kw: (taco.matmul_fp8(a, b, c, d, **kw),), [xq, xs, wq, ws]),
+        (lambda a, b, c, d, **kw: (taco.matmul_fp8(*taco.quantize_rows(dy, **kw), c, d, **kw), a, b), [xq, xs, wqt, wst]),
+        (lambda a, b, c, **kw: (taco.wgrad_fp8(a, b, c, k, **kw),), [dy, xq, xs]),
+        (lambda a, **kw: taco.swiglu_quantize(a, **kw), [gu]),
+        (lambda a, b, c, **kw: taco.swiglu_backward(a, b, c, **kw), [dh, cq, cs]),
+    ]
+
+
+SHAPES = [(5, 300, 256), (200, 384, 640), (33, 77, 301)]
+
+
+@pytest.mark.parametrize("t,n,k", SHAPES)
+def test_strided_and_misaligned_arguments(t, n, k):
+    for call, given in calls(t, n, k):
+        want = call(*given)
+        for at in range(len(given)):
+            for view in strided(given[at]):
+                got = call(*given[:at], view, *given[at + 1:])
+                assert all(torch.equal(a, b) for a, b in zip(got, want))
+        for kind in range(2):
+            got = call(*(strided(a)[kind] for a in given))
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("t,n,k", SHAPES)
+def test_every_operator_on_another_stream(t, n, k):
+    stream = torch.cuda.Stream()
+    for call, given in calls(t, n, k):
+        want = call(*given)
+        views = [strided(a)[0] for a in given]
+        torch.cuda.synchronize()
+        plain, copied = call(*given, stream=stream), call(*views, stream=stream)
+        stream.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(plain, want))
+        assert all(torch.equal(a, b) for a, b in zip(copied, want))
+
+
+# ----------------------------------------------------------------------- graphs
+
+def test_graphs_of_calls_with_workspaces():
+    """Split product, split and widened weight gradients, added to, and the norm's gradients; replayed with new inputs,
+    with eager work between the replays."""
+    shapes = ((300, 512, 8192), (2000, 200, 300), (700, 4096, 4090), (40, 1600, 1600))
+    given = [layer(*s) for s in shapes]
+    z = [activations(300, 1600, 1), activations(70, 20000, 2)]
+    rstd = [torch.rsqrt(v.float().square().mean(1) + 1e-5) for v in z]
+    sums = [torch.zeros(s[1], s[2], device="cuda") for s in shapes]
+
+    def step(sums):
+        out = []
+        for (t, n, k), (x, dy, xq, w, wt), dw in zip(shapes, given, sums):
+            q = taco.quantize_rows(x, q=xq[0], scale=xq[1])
+            out += [taco.matmul_fp8(*q, *w), taco.matmul_fp8(*taco.quantize_rows(dy), *wt),
+                    taco.wgrad_fp8(dy, *q, k), taco.wgrad_fp8(dy, *q, k, dw=dw, accumulate=True)]
+        for v, r in zip(z, rstd):
+            out += taco.rmsnorm_backward(v, v, r, v[0])
+        return out
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step([s.clone() for s in sums])
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        held = step(sums)
+    for replay in range(4):
+        for (t, n, k), (x, dy, _, _, _) in zip(shapes, given):
+            x.copy_(activations(t, k, 100 + replay))
+            dy.copy_(activations(t, n, 200 + replay))
+        for v in z:
+            v.copy_(activations(*v.shape, 300 + replay))
+        before = [s.clone() for s in sums]
+        want = [v.clone() for v in step(before)]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, held)), replay
