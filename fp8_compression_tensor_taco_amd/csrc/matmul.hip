@@ -1005,27 +1005,25 @@ __global__ __launch_bounds__(512) void wgrad_turns_kernel(const WgradArgs p) {
     }
     if constexpr (!group.value) meet();
   };
-  if (steps > 0) {
 #pragma unroll
-    for (int i = 0; i < D::N; ++i) load_d(0, i);
+  for (int i = 0; i < D::N; ++i) load_d(0, i);
 #pragma unroll
-    for (int i = 0; i < X::N; ++i) load_x(0, i);
+  for (int i = 0; i < X::N; ++i) load_x(0, i);
 #pragma unroll
-    for (int i = 0; i < D::N; ++i) {
-      store_d(0, i);
-      load_d(1, i);
-    }
-#pragma unroll
-    for (int i = 0; i < X::N; ++i) {
-      store_x(0, i);
-      load_x(1, i);
-    }
-    reads_done_and_meet();
-    if (wave >= 4)
-      run(std::true_type{});
-    else
-      run(std::false_type{});
+  for (int i = 0; i < D::N; ++i) {
+    store_d(0, i);
+    load_d(1, i);
   }
+#pragma unroll
+  for (int i = 0; i < X::N; ++i) {
+    store_x(0, i);
+    load_x(1, i);
+  }
+  reads_done_and_meet();
+  if (wave >= 4)
+    run(std::true_type{});
+  else
+    run(std::false_type{});
   const int t0 = steps * kTokens;
   if (t0 < p.tokens) {
     x.load(thread, p.q, p.scale, t0, p.tokens, k0, p.kcols, p.kscales);
@@ -1146,59 +1144,57 @@ __global__ __launch_bounds__(256) void wgrad_copies_kernel(const WgradArgs p, co
   auto read_x = [&](int odd, int i) {
     (i < KR ? fx[i] : fx_last[odd][i - KR]) = read_columns<B>(lds + 2 * odd * kChunkBytes, at_x[i], 0, 0);
   };
-  if (chunks > 0) {
 #pragma unroll
-    for (int c = 0; c < kChunkRing; ++c) {
+  for (int c = 0; c < kChunkRing; ++c) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) copy(c & 1, i);
-      copied_chunk();
-      if (c & 1) to ^= kPair;
+    for (int i = 0; i < 8; ++i) copy(c & 1, i);
+    copied_chunk();
+    if (c & 1) to ^= kPair;
+  }
+  copies_left<8 * (kChunkRing - 2)>();
+  meet();
+#pragma unroll
+  for (int i = 0; i < NT; ++i) read_d(0, i);
+#pragma unroll
+  for (int i = 0; i < KT; ++i) read_x(0, i);
+  reads_done();
+  meet();
+  auto chunk = [&](auto odd_) {
+    constexpr int odd = odd_;
+    fence();
+    if constexpr (odd) {
+#pragma unroll
+      for (int i = 0; i < KT; ++i) {
+        at_x[i] ^= kPair;
+        at_d[i] ^= kPair;
+      }
     }
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        multiply_into(i < KR ? fx[i] : fx_last[odd][i - KR], fd[odd][j], acc[i][j]);
+        fence();
+        if (i == 0)
+          read_d(odd ^ 1, j);
+        else if (i == 1 && j < KT - KR)
+          read_x(odd ^ 1, KR + j);
+        else if (j == 2 && i <= KR)
+          read_x(odd ^ 1, i - 1);
+        if (j == 5) copy(odd, i);
+        fence();
+      }
+    copied_chunk();
+    reads_done();
     copies_left<8 * (kChunkRing - 2)>();
     meet();
-#pragma unroll
-    for (int i = 0; i < NT; ++i) read_d(0, i);
-#pragma unroll
-    for (int i = 0; i < KT; ++i) read_x(0, i);
-    reads_done();
-    meet();
-    auto chunk = [&](auto odd_) {
-      constexpr int odd = odd_;
-      fence();
-      if constexpr (odd) {
-#pragma unroll
-        for (int i = 0; i < KT; ++i) {
-          at_x[i] ^= kPair;
-          at_d[i] ^= kPair;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < KT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          multiply_into(i < KR ? fx[i] : fx_last[odd][i - KR], fd[odd][j], acc[i][j]);
-          fence();
-          if (i == 0)
-            read_d(odd ^ 1, j);
-          else if (i == 1 && j < KT - KR)
-            read_x(odd ^ 1, KR + j);
-          else if (j == 2 && i <= KR)
-            read_x(odd ^ 1, i - 1);
-          if (j == 5) copy(odd, i);
-          fence();
-        }
-      copied_chunk();
-      reads_done();
-      copies_left<8 * (kChunkRing - 2)>();
-      meet();
-      if constexpr (odd) to ^= kPair;
-    };
-    for (int c = 0; c < chunks; c += 2) {
-      chunk(std::integral_constant<int, 0>{});
-      chunk(std::integral_constant<int, 1>{});
-    }
-    copies_left<0>();
+    if constexpr (odd) to ^= kPair;
+  };
+  for (int c = 0; c < chunks; c += 2) {
+    chunk(std::integral_constant<int, 0>{});
+    chunk(std::integral_constant<int, 1>{});
   }
+  copies_left<0>();
   const int t0 = chunks * kChunk;
   if (t0 < p.tokens) {                             // what is left over, widened on its way
     X x;
@@ -1368,9 +1364,8 @@ int64_t widened_rows(int64_t tokens) { return tokens / kTokens * kTokens; }
 
 void launch_wgrad_copies(const WgradArgs& p, uint16_t* wide, hipStream_t stream) {
   const int64_t rows = widened_rows(p.tokens);
-  if (rows > 0)
-    hipLaunchKernelGGL(widen_rows_kernel, dim3(static_cast<unsigned>((rows * (p.kcols / 16) + 255) / 256)), dim3(256), 0,
-                       stream, p.q, p.scale, rows, p.kcols, p.kscales, wide);
+  hipLaunchKernelGGL(widen_rows_kernel, dim3(static_cast<unsigned>((rows * (p.kcols / 16) + 255) / 256)), dim3(256), 0,
+                     stream, p.q, p.scale, rows, p.kcols, p.kscales, wide);
   hipLaunchKernelGGL(wgrad_copies_kernel, dim3(static_cast<unsigned>(tiles_of(p.n, p.k, 256, 256))), dim3(256), 0,
                      stream, p, wide);
 }
@@ -1383,7 +1378,8 @@ void launch_wgrad_copies(const WgradArgs& p, uint16_t* wide, hipStream_t stream)
 // 0.75, 650: 1.7); 256 x 256 tiles 1.7 a round of 256, or 1.45 and the widening
 // where rows of dy are aligned, and 8 for a round's stores, which nothing
 // overlaps (256 x 8192 x 8192: 79 against 70 with 128 x 128).  Partial sums cost their
-// traffic at 4.5 TB/s and a launch.
+// traffic at 4.5 TB/s and a launch.  Below seven steps the estimate of 256 x 256
+// tiles is above that of 128 x 128 at any size; their kernels count on whole steps.
 struct WgradPlan {
   int tile, splits, split_steps;
 };
@@ -1392,9 +1388,10 @@ WgradPlan wgrad_plan(int64_t tokens, int64_t n, int64_t k) {
   const int64_t t64 = tiles_of(n, k, 64, 64), t128 = tiles_of(n, k, 128, 128), t256 = tiles_of(n, k, 256, 256);
   WgradPlan best{256, 1, static_cast<int>(steps)};
   const double rounds = static_cast<double>((t256 + 255) / 256);
-  double least = n % 8 == 0 ? 4 + (8 + 1.45 * static_cast<double>(steps)) * rounds + 0.6e-6 * static_cast<double>(tokens * k)
-               : n >= 8     ? 4 + (8 + 1.7 * static_cast<double>(steps)) * rounds
-                            : 1e30;
+  double least = 1e30;
+  if (n >= 8 && steps >= 7)
+    least = n % 8 == 0 ? 4 + (8 + 1.45 * static_cast<double>(steps)) * rounds + 0.6e-6 * static_cast<double>(tokens * k)
+                       : 4 + (8 + 1.7 * static_cast<double>(steps)) * rounds;
   for (int splits = 1; splits <= 32 && (splits == 1 || splits * 4 <= steps); ++splits) {
     const int64_t each = (steps + splits - 1) / splits;
     if ((steps + each - 1) / each != splits) continue;
