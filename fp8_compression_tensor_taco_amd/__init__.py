@@ -3,7 +3,8 @@
 Python face of libtaco (include/taco.h): ``compress``, ``decompress`` and
 ``decompress_sum`` over bf16 [tokens, hidden] GPU tensors, and the operators of
 an 8-bit linear layer (include/taco_linear.h): block-scaled FP8 quantisation,
-norm, matrix product, gradients and gated unit.  The library is loaded on first use and the calls raise if it is missing; there is no CPU path.
+norm, matrix product, gradients and gated unit.  The library is loaded on first
+use and the calls raise if it is missing; there is no CPU path.
 """
 from ._binding import (  # noqa: F401
     TACO_AMAX_FLOATS,

@@ -18,9 +18,11 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 // columns of 16 rows of both operands, one block each, and multiplies the two
 // blocks' scales in, so the whole sum over k stays in one fp32 accumulator and
 // the scales cost no vector instruction.  (The instruction aligns the products
-// of eight consecutive columns to the largest of them and keeps 13 bits below
-// it: a relative error near 3e-5 on normal data, under the 2^-9 of the output's
-// rounding.)  b is the first operand, so a lane ends with four consecutive n of
+// of eight consecutive columns to the largest of them, keeps 13 bits below
+// it, and cuts where it accumulates: a relative error near 3e-5 on normal data,
+// under the 2^-9 of the output's rounding.  That is what the
+// instruction keeps, in the library's FP8 product as well; products of codes
+// widened to bf16 would keep more and take twice the time.)  b is the first operand, so a lane ends with four consecutive n of
 // one row of y.
 
 __device__ __forceinline__ unsigned lds_address(const void* p) {
@@ -337,11 +339,15 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void matmul_tiles_kernel(
 
 // Few rows of a (at most 16 MT): every byte of b is used once, so the weight's
 // stream from HBM is the time.  A workgroup takes 16 rows of b and its
-// wavefronts split k, each reading its fragments straight into registers,
-// kAhead steps at a time; the partial sums are added in LDS in the wavefronts'
-// order.  No barrier but that one, no copy through LDS.  4 x 4096 x 4096: 5.4 us
-// over weights that are in the last-level cache (3.1 TB/s; launch and latency are
-// about half of it), 1 x 14336 x 3584: 12.0 us (4.3 TB/s).
+// wavefronts split k, each reading its fragments straight into registers, in
+// turns of kAhead steps; the partial sums are added in LDS in the wavefronts'
+// order.  No barrier but that one, no copy through LDS.  The loads of a turn are
+// not all ahead of its products: the compiler moves those of the last of the
+// four steps (MT 1), or of all but the first (MT 2), behind the first product
+// and into the branches around the others, so that a turn waits for memory
+// twice.  Kernel durations, median: 4 x 4096 x 4096: 5.5 us over weights that
+// are in the last-level cache (3.1 TB/s; launch and the two latencies are
+// most of it), 1 x 14336 x 3584: 11.6 us (4.4 TB/s), 32 x 4096 x 4096: 10.0.
 constexpr int kFewWaves = 8;
 template <int MT>
 __global__ __launch_bounds__(64 * kFewWaves) void matmul_few_kernel(
@@ -448,9 +454,12 @@ __device__ __forceinline__ void reads_done() {
 // and waits until only the copies of the last two halves (eight each) are in
 // flight.  Operations issued later only make a wait stricter.
 //
-// 8192 x 8192 x 8192: 365 us, 3.0 PFLOP/s; 8192 x 14336 x 3584: 313 us, 2.7 (on
-// the same card 392 and 331 with eight wavefronts of 64 x 128 that take turns
-// and a third more LDS reads).  Of the 365, 285 are the matrix instructions at
+// 8192 x 8192 x 8192: 365 us, 3.0 PFLOP/s; 8192 x 14336 x 3584: 315 us, 2.7 (on
+// one card 392 and 331, against 365 and 313, with eight wavefronts of 64 x 128
+// that take turns and a third more LDS reads).  These are at the upper end of the
+// clock, p10 of a trace or calls among lighter work; where such products follow
+// each other the clock falls, and the medians of the trace are 410 us (2.7
+// PFLOP/s) and 359.  Of the 365, 285 are the matrix instructions at
 // the clock they run at; the copies add 63 to them and the reads 15 to 18.  The copies'
 // cost is not their latency (waiting for fewer of them changes nothing), and
 // spreading them over the half steps does not lower it.  A tile's start and
@@ -816,11 +825,14 @@ struct StepMover {
 };
 
 // Tiles of BN = 16 NT WN rows by BK = 16 KT WK columns of dw, two steps in LDS
-// and the global loads of the next two in registers.  Eight wavefronts for 128 x
+// and the global loads of the next two issued ahead.  Eight wavefronts for 128 x
 // 128: a step of one workgroup per CU waits less with two wavefronts per SIMD
-// than with one (1021 x 1600 x 1600: 15.6 against 17.4 us).  At that size 169 of
-// 256 CUs have a tile and a step costs 0.65 us, of which the matrix instructions
-// are 0.12: latency.
+// than with one (1021 x 1600 x 1600: 15.6 against 17.4 us).  At that size (16.5
+// us, median of a trace) 169 of 256 CUs have a tile and a step costs 0.65 us, of
+// which the matrix instructions are 0.12; the rest is latency.  Part of that is
+// the code's: the loads stand under a condition, so the compiler cannot count
+// what is in flight at the loop's head, and the first step of each pair waits
+// for both steps' loads.
 template <int KT, int NT, int WK, int WN, DyRows ROWS>
 __global__ __launch_bounds__(64 * WK * WN) void wgrad_tiles_kernel(const WgradArgs p) {
   constexpr int BK = 16 * KT * WK, BN = 16 * NT * WN, kThreads = 64 * WK * WN;
@@ -940,9 +952,11 @@ __device__ __forceinline__ void store_wgrad_tile(const WgradArgs& p, uint8_t* mi
 // hold nothing but the reads, and whole steps need no check of rows and one
 // offset per operand (a thread's pieces are a fixed number of rows apart); the
 // rows that are left over follow as one step of their own, without turns.
-// 4096 x 16384 x 4096: 465 to 485 us on different cards, 1.13 to 1.18 PFLOP/s; the
-// stores to LDS account for about 43 us of it, the loads for 80, the end of the
-// tiles for 40.  Loads in M1, or both loads and stores later, made no difference.
+// 4096 x 16383 x 4096: 585 us, 0.94 PFLOP/s (median of a trace; 619 between other
+// large products).  With dy's rows aligned (16384 columns) it took 465 to 485 on
+// different cards, of which the stores to LDS account for about 43 us, the loads
+// for 80, the end of the tiles for 40.  Loads in M1, or both loads and stores
+// later, made no difference.
 __global__ __launch_bounds__(512) void wgrad_turns_kernel(const WgradArgs p) {
   constexpr int KT = 8, NT = 4, B = 256, kThreads = 512;
   using Tile = TokenTile<B>;
@@ -1077,7 +1091,11 @@ __global__ __launch_bounds__(256) void widen_rows_kernel(const uint8_t* __restri
 //
 // 4096 x 16384 x 4096: 418 us with the widening, 1.32 PFLOP/s, against 490 on
 // the same card for wgrad_turns_kernel; 8192 x 8192 x 8192: 803 (1.37) against 942.
-// With the accumulators left to the compiler it takes 473.
+// With the accumulators left to the compiler it takes 473.  These are at the upper
+// end of the clock (p10 of a trace: 410 and 15 for the widening, 785 and 35);
+// the trace's medians are 430 and 15, 816 and 37, and 461 and 14 between
+// other large products.  Adding to dw costs its reading, not overlapped:
+// 560 us against 466 on one card.
 constexpr int kChunk = 32, kChunkRing = 4;
 constexpr int kChunkBytes = kChunk * 512;        // of 256 columns of an operand
 
@@ -1317,6 +1335,9 @@ void launch_big(const MatmulArgs& p, hipStream_t stream) {
 //   4608  4096  4096                           106           87.9          82.5
 //   8192  4224  512                            44.9          29.5          37.0
 //   8192  3584  1000   99.4        56.6        50.0          37.6          33.1
+// (KG 2 of 64 x 64 has a ring of four steps and one workgroup to a CU, KG 1 a ring of
+// three and three to a CU; at 257 to 512 tiles no CU has more than two, and other
+// rings were not measured there.)
 // so 64 x 64 tiles until a CU would have more than three, two groups of
 // wavefronts for a tile where a CU has one; 128 x 128 while their workgroups
 // are all resident (two to a CU), and 256 x 256 from there on, which loses up to
@@ -1372,13 +1393,16 @@ void launch_wgrad_copies(const WgradArgs& p, uint16_t* wide, hipStream_t stream)
 
 // Which kernel, and over how many runs of tokens whose partial sums go through
 // the workspace: the least of these estimates of its time in microseconds.  Per
-// step of 64 tokens, measured: 64 x 64 tiles 0.37 while there are few
-// workgroups and 0.12 + 1 / 1050 each then (169: 0.37, 650: 0.75, 1024: 1.05,
+// step of 64 tokens: 64 x 64 tiles 0.37 while there are few workgroups and 0.12 +
+// 1 / 1050 each then (measured, workgroups: us: 169: 0.37, 650: 0.75, 1024: 1.05,
 // 4096: 3.6); 128 x 128 tiles 0.65 and from 254 on 1 / 390 each (169: 0.63, 256:
-// 0.75, 650: 1.7); 256 x 256 tiles 1.7 a round of 256, or 1.45 and the widening
-// where rows of dy are aligned, and 8 for a round's stores, which nothing
-// overlaps (256 x 8192 x 8192: 79 against 70 with 128 x 128).  Partial sums cost their
-// traffic at 4.5 TB/s and a launch.  Below seven steps the estimate of 256 x 256
+// 0.75, 650: 1.7), which fits those points to 13 %; 256 x 256 tiles 1.7 a round
+// of 256, or 1.45 and the widening where rows of dy are aligned, and 8 for a
+// round's stores, which nothing overlaps.  Partial sums cost their traffic at 4.5
+// TB/s and a launch.  The estimates leave out the stores of the smaller tiles and
+// the start of the larger, so few steps over a large dw come out too low: 256 x
+// 8192 x 8192 46 against 84 measured (70 in an earlier run, and 79 there with 256 x
+// 256 tiles), 512 x 4096 x 4096 25 against 33.  Below seven steps the estimate of 256 x 256
 // tiles is above that of 128 x 128 at any size; their kernels count on whole steps.
 struct WgradPlan {
   int tile, splits, split_steps;

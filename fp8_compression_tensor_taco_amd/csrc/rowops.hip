@@ -31,8 +31,9 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // One wavefront for each 512 * CH columns of a row: no reduction goes beyond 16
 // lanes, so the waves are as many as the CUs can hold and nothing waits but the
-// loads.  4096 x 16384: 43 us, 4.7 TB/s; 8192 x 8191 (element-aligned rows): 42
-// us, 4.7; up to a few hundred KB a launch, 4 us.
+// loads.  4096 x 16384: 43 us, 4.7 TB/s, between other large calls, 32 in a row of
+// its own (part of its traffic stays in the last-level cache); 8192 x 8191
+// (element-aligned rows): 40 us, 5.0; up to a few hundred KB a launch, 4 us.
 template <int CH, bool WIDE>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const uint16_t* __restrict__ x, int64_t rows,
                                                                  int cols, int segments, uint8_t* __restrict__ q,
@@ -140,7 +141,9 @@ __global__ __launch_bounds__(kThreads) void quantize_weight_kernel(const uint16_
 //
 // z = bf16(x + residual), rstd = 1 / sqrt(mean(z^2) + eps), the codes those of
 // z * rstd * weight.  4096 x 4096 with a residual: 24 us, 4.9 TB/s; 8192 x 8000:
-// 85 us, 5.4; 8 x 4096: 5 us, latency.
+// 84 us, 5.5; 8 x 4096: 4.6 us, latency.  The weight's chunks are loaded one by one
+// behind the row's sum, each behind the stores of the one before: many rows
+// hide that, a single one waits for every chunk.
 template <int WPR>
 struct RowGroup {
   static constexpr int kWG = WPR == 1 ? kThreads : 64 * WPR;
@@ -224,7 +227,8 @@ __global__ __launch_bounds__(RowGroup<WPR>::kWG) void rmsnorm_quantize_kernel(
 // `partial`, and column_sums_kernel adds the workgroups' rows in order.  Two
 // rows at a time and two or more workgroups per CU keep the loads going across
 // the rows' reductions.  8192 x 3584: 43 us, 5.5 TB/s, and 5 for the column
-// sums; 1021 x 1600: 6.7 and 3.8, latency.
+// sums; 1021 x 1600: 6.4 and 3.7, latency (one turn, whose loads are issued only
+// when the weight has arrived).
 //
 // The multiply-adds are written out, so that a row's result does not depend on
 // its place or on the kernel that computes it.
@@ -320,8 +324,8 @@ __global__ __launch_bounds__(64 * WAVES) void rmsnorm_backward_kernel(
 
 // Rows too long for that: first mean(dy * weight * xhat) of each row, a
 // workgroup per row, then the rest by pieces of 2048 columns.  dy and z are read
-// twice, the second time mostly from the last-level cache: 1000 x 20000 in 38 us,
-// 3.1 TB/s.
+// twice, the second time mostly from the last-level cache: 1000 x 20000 without
+// dz in 13 and 19 us, and 6 for the column sums, 3.1 TB/s in all.
 template <bool WIDE>
 __global__ __launch_bounds__(kThreads) void rmsnorm_row_means_kernel(
     const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, const float* __restrict__ rstd,
@@ -407,12 +411,15 @@ __global__ __launch_bounds__(4 * kSumClasses) void column_sums_kernel(const floa
 
 // ---------------------------------------------------------------- gated unit
 
-// exp(-g) may be infinite: 1 / (1 + inf) = 0.
+// exp(-g) may be infinite: 1 / (1 + inf) = 0.  The hardware's exp2 of the scaled
+// argument: a relative error of at most (|g| + 12) 2^-24, as the argument's
+// rounding grows with it, which is far below the codes' and bf16's; below g = -88.7
+// the result is 0 where sigmoid is under 2^-127.
 __device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
 
 // h = g * sigmoid(g) * u.  One wavefront for each 512 * CH columns of a row's
 // gate and the same of its up part.  4096 tokens, inner 8192: 46 us, 5.1 TB/s;
-// inner 5461 (element-aligned up parts): 41 us, 3.8.
+// inner 5440: 34 us, 4.5; inner 5461 (element-aligned up parts): 43 us, 3.6.
 template <int CH, bool WIDE>
 __global__ __launch_bounds__(kThreads) void swiglu_quantize_kernel(const uint16_t* __restrict__ gu, int64_t rows,
                                                                    int inner, int segments, uint8_t* __restrict__ hq,
@@ -516,7 +523,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
 // start of du, so a lane computes the 8 output columns it holds: all of dg or
 // all of du, from 8 columns of dh and of the checkpoint at any alignment and in
 // at most two blocks, or, where the two meet and at the end, one by one.  It reads
-// dh and the checkpoint twice: 4096 tokens, inner 5440: 68 us, 3.3 TB/s.
+// dh and the checkpoint and computes both gradients twice, and stores one: 4096
+// tokens, inner 5440: 63 us, 3.6 TB/s; 5461: 68 us, 3.3.
 __global__ __launch_bounds__(kThreads) void swiglu_backward_any_kernel(
     const uint16_t* __restrict__ dh, const uint8_t* __restrict__ cq, const uint8_t* __restrict__ cs, int64_t rows,
     int inner, int segments, uint16_t* __restrict__ dgu, uint8_t* __restrict__ dq, uint8_t* __restrict__ ds) {
