@@ -39,6 +39,13 @@ _SIGNATURES = {
     "taco_wgrad_fp8": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, ctypes.c_int32, _vp, _size, _vp]),
     "taco_swiglu_quantize": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
     "taco_swiglu_backward": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "taco_linear_fp8_workspace_bytes": (_size, [_i64, _i64, _i64]),
+    "taco_linear_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int32, _i64, _i64, _i64, _vp, _vp, _size, _vp]),
+    "taco_linear_quantize_workspace_bytes": (_size, [_i64, _i64, _i64]),
+    "taco_linear_quantize": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, ctypes.c_int32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp,
+                                            _size, _vp]),
+    "taco_activation_backward_workspace_bytes": (_size, [_i64, _i64]),
+    "taco_activation_backward": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int32, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _size, _vp]),
 }
 _typed = None
 _native = None
@@ -103,6 +110,18 @@ def matmul_fp8_workspace_bytes(m: int, n: int, k: int) -> int:
 
 def wgrad_fp8_workspace_bytes(tokens: int, n: int, cols: int) -> int:
     return int(_lib().taco_wgrad_fp8_workspace_bytes(tokens, n, cols))
+
+
+def linear_fp8_workspace_bytes(m: int, n: int, k: int) -> int:
+    return int(_lib().taco_linear_fp8_workspace_bytes(m, n, k))
+
+
+def linear_quantize_workspace_bytes(m: int, n: int, k: int) -> int:
+    return int(_lib().taco_linear_quantize_workspace_bytes(m, n, k))
+
+
+def activation_backward_workspace_bytes(tokens: int, cols: int) -> int:
+    return int(_lib().taco_activation_backward_workspace_bytes(tokens, cols))
 
 
 # Every call with a stream makes it current and calls itself: outputs, copies of
@@ -214,3 +233,47 @@ def swiglu_backward(dh: torch.Tensor, cq: torch.Tensor, cs: torch.Tensor, *, qua
         with _on(stream):
             return swiglu_backward(dh, cq, cs, quantize=quantize, dgu=dgu, dq=dq, ds=ds)
     return _binding().swiglu_backward(dh, cq, cs, quantize, dgu, dq, ds, _current(dh))
+
+
+def linear_fp8(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Tensor, *, bias: torch.Tensor | None = None,
+               activation: str | None = None, residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """bf16 [m, n] = act(a b^T + bias) + residual, with matmul_fp8's operands and sums and one rounding at the end.
+
+    bias bf16 [n] and residual bf16 [m, n] may be left out; activation is None, 'relu', 'gelu' (through the normal
+    distribution function), 'gelu_tanh' or 'silu'."""
+    if stream is not None:
+        with _on(stream):
+            return linear_fp8(qa, sa, qb, sb, bias=bias, activation=activation, residual=residual, out=out, workspace=workspace)
+    return _binding().linear_fp8(qa, sa, qb, sb, bias, activation, residual, out, workspace, _current(qa))
+
+
+def linear_quantize(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Tensor, *, bias: torch.Tensor | None = None,
+                    activation: str | None = None, checkpoint: bool = True, hq: torch.Tensor | None = None,
+                    hs: torch.Tensor | None = None, cq: torch.Tensor | None = None, cs: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """linear_fp8 without a residual, quantised: h = act(t), t = a b^T + bias.
+
+    Returns (hq, hs, cq, cs): h in the block format, and t in 8 bits for activation_backward (None for those with
+    checkpoint=False, and without an activation, whose gradient needs no t)."""
+    if stream is not None:
+        with _on(stream):
+            return linear_quantize(qa, sa, qb, sb, bias=bias, activation=activation, checkpoint=checkpoint, hq=hq, hs=hs,
+                                   cq=cq, cs=cs, workspace=workspace)
+    return _binding().linear_quantize(qa, sa, qb, sb, bias, activation, checkpoint, hq, hs, cq, cs, workspace, _current(qa))
+
+
+def activation_backward(dh: torch.Tensor, cq: torch.Tensor | None, cs: torch.Tensor | None, activation: str | None, *,
+                        quantize: bool = True, bias: bool = True, dt: torch.Tensor | None = None,
+                        dq: torch.Tensor | None = None, ds: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None):
+    """Gradient of linear_quantize's nonlinearity and bias for dh bf16 [tokens, cols], at the checkpoint's t.
+
+    Returns (dt, dq, ds, dbias): dt = dh act'(t) in bf16 (dh itself without an activation, whose checkpoint is None),
+    the same in the block format for the gradients of the product (None with quantize=False), and its sums over tokens
+    in fp32, the bias's gradient (None with bias=False)."""
+    if stream is not None:
+        with _on(stream):
+            return activation_backward(dh, cq, cs, activation, quantize=quantize, bias=bias, dt=dt, dq=dq, ds=ds,
+                                       dbias=dbias, workspace=workspace)
+    return _binding().activation_backward(dh, cq, cs, activation, quantize, bias, dt, dq, ds, dbias, workspace, _current(dh))

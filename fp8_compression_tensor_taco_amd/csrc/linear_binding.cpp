@@ -243,6 +243,107 @@ py::tuple swiglu_backward(const Tensor& dh_, const Tensor& cq_, const Tensor& cs
   return py::make_tuple(dgu, maybe(dq), maybe(ds));
 }
 
+// A nonlinearity's name, or None.
+int32_t activation_of(const std::optional<std::string>& name) {
+  if (!name) return TACO_ACT_NONE;
+  if (*name == "relu") return TACO_ACT_RELU;
+  if (*name == "gelu") return TACO_ACT_GELU;
+  if (*name == "gelu_tanh") return TACO_ACT_GELU_TANH;
+  if (*name == "silu") return TACO_ACT_SILU;
+  throw py::value_error("activation must be None, 'relu', 'gelu', 'gelu_tanh' or 'silu', got '" + *name + "'");
+}
+
+// The operands of a product with an epilogue.
+struct Product {
+  Tensor qa, sa, qb, sb, bias;
+  int64_t m, n, k;
+  at::Device device;
+  Product(const Tensor& qa_, const Tensor& sa_, const Tensor& qb_, const Tensor& sb_, const Given& bias_)
+      : qa(input(qa_, "qa", at::kByte)), qb(input(qb_, "qb", at::kByte)), m(qa.size(0)), n(qb.size(0)), k(qa.size(1)),
+        device(qa.device()) {
+    if (k == 0 || k % kBlock != 0 || qb.size(1) != k)
+      throw py::value_error("qa and qb must have the same number of columns, a multiple of 128: got " +
+                            std::to_string(k) + " and " + std::to_string(qb.size(1)));
+    sa = input(sa_, "sa", at::kByte, {m, fp8_scale_cols(k)}, device);
+    sb = input(sb_, "sb", at::kByte, {fp8_cols(n) / kBlock, fp8_scale_cols(k)}, device);
+    if (qb.device() != device) throw py::value_error("all tensors must be on the same device");
+    if (bias_) bias = input(*bias_, "bias", at::kBFloat16, {n}, device);
+  }
+};
+
+const void* maybe_data(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+Tensor linear_fp8(const Tensor& qa, const Tensor& sa, const Tensor& qb, const Tensor& sb, const Given& bias,
+                  const std::optional<std::string>& activation, const Given& residual_, const Given& out_,
+                  const Given& workspace_, uint64_t stream) {
+  const int32_t act = activation_of(activation);
+  const Product p(qa, sa, qb, sb, bias);
+  Tensor residual;
+  if (residual_) residual = input(*residual_, "residual", at::kBFloat16, {p.m, p.n}, p.device);
+  const Tensor out = output(out_, "out", at::kBFloat16, {p.m, p.n}, p.device);
+  const Workspace ws(workspace_, taco_linear_fp8_workspace_bytes(p.m, p.n, p.k), p.device);
+  check(taco_linear_fp8(bytes_of(p.qa), bytes_of(p.sa), bytes_of(p.qb), bytes_of(p.sb), maybe_data(p.bias),
+                        maybe_data(residual), act, p.m, p.n, p.k, out.data_ptr(), ws.at, ws.bytes, stream_of(stream)));
+  return out;
+}
+
+py::tuple linear_quantize(const Tensor& qa, const Tensor& sa, const Tensor& qb, const Tensor& sb, const Given& bias,
+                          const std::optional<std::string>& activation, bool checkpoint, const Given& hq_,
+                          const Given& hs_, const Given& cq_, const Given& cs_, const Given& workspace_,
+                          uint64_t stream) {
+  const int32_t act = activation_of(activation);
+  const Product p(qa, sa, qb, sb, bias);
+  const int64_t wide = fp8_cols(p.n), scales = fp8_scale_cols(p.n);
+  const Tensor hq = output(hq_, "hq", at::kByte, {p.m, wide}, p.device);
+  const Tensor hs = output(hs_, "hs", at::kByte, {p.m, scales}, p.device);
+  Tensor cq, cs;
+  if (checkpoint && act != TACO_ACT_NONE) {
+    cq = output(cq_, "cq", at::kByte, {p.m, wide}, p.device);
+    cs = output(cs_, "cs", at::kByte, {p.m, scales}, p.device);
+  } else if (cq_ || cs_) {
+    throw py::value_error("cq and cs are outputs of checkpoint=True with an activation");
+  }
+  const Workspace ws(workspace_, taco_linear_quantize_workspace_bytes(p.m, p.n, p.k), p.device);
+  check(taco_linear_quantize(bytes_of(p.qa), bytes_of(p.sa), bytes_of(p.qb), bytes_of(p.sb), maybe_data(p.bias), act,
+                             p.m, p.n, p.k, bytes_of(hq), bytes_of(hs), maybe_bytes(cq), maybe_bytes(cs), ws.at,
+                             ws.bytes, stream_of(stream)));
+  return py::make_tuple(hq, hs, maybe(cq), maybe(cs));
+}
+
+py::tuple activation_backward(const Tensor& dh_, const Given& cq_, const Given& cs_,
+                              const std::optional<std::string>& activation, bool quantize, bool bias, const Given& dt_,
+                              const Given& dq_, const Given& ds_, const Given& dbias_, const Given& workspace_,
+                              uint64_t stream) {
+  const int32_t act = activation_of(activation);
+  const Tensor dh = input(dh_, "dh", at::kBFloat16);
+  const int64_t tokens = dh.size(0), cols = dh.size(1);
+  const at::Device device = dh.device();
+  Tensor cq, cs, dt, dq, ds, dbias;
+  if (act != TACO_ACT_NONE) {
+    if (!cq_ || !cs_) throw py::value_error("cq and cs, the checkpoint, are needed with an activation");
+    cq = input(*cq_, "cq", at::kByte, {tokens, fp8_cols(cols)}, device);
+    cs = input(*cs_, "cs", at::kByte, {tokens, fp8_scale_cols(cols)}, device);
+    dt = output(dt_, "dt", at::kBFloat16, {tokens, cols}, device);
+  } else if (cq_ || cs_ || dt_) {
+    throw py::value_error("without an activation there is no checkpoint, and dt is dh itself");
+  }
+  if (quantize) {
+    dq = output(dq_, "dq", at::kByte, {tokens, fp8_cols(cols)}, device);
+    ds = output(ds_, "ds", at::kByte, {tokens, fp8_scale_cols(cols)}, device);
+  } else if (dq_ || ds_) {
+    throw py::value_error("dq and ds are outputs of quantize=True");
+  }
+  if (bias)
+    dbias = output(dbias_, "dbias", at::kFloat, {cols}, device);
+  else if (dbias_)
+    throw py::value_error("dbias is an output of bias=True");
+  const Workspace ws(workspace_, bias ? taco_activation_backward_workspace_bytes(tokens, cols) : 0, device);
+  check(taco_activation_backward(dh.data_ptr(), maybe_bytes(cq), maybe_bytes(cs), act, tokens, cols,
+                                 dt.defined() ? dt.data_ptr() : nullptr, maybe_bytes(dq), maybe_bytes(ds),
+                                 dbias.defined() ? floats_of(dbias) : nullptr, ws.at, ws.bytes, stream_of(stream)));
+  return py::make_tuple(dt.defined() ? dt : dh_, maybe(dq), maybe(ds), maybe(dbias));
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_linear_binding, m) {
@@ -254,4 +355,7 @@ PYBIND11_MODULE(_linear_binding, m) {
   m.def("wgrad_fp8", &wgrad_fp8);
   m.def("swiglu_quantize", &swiglu_quantize);
   m.def("swiglu_backward", &swiglu_backward);
+  m.def("linear_fp8", &linear_fp8);
+  m.def("linear_quantize", &linear_quantize);
+  m.def("activation_backward", &activation_backward);
 }

@@ -1,9 +1,10 @@
 // The matrix products of the 8-bit linear layer (taco_linear.h) for gfx950:
-// the FP8 product of quantised rows with a quantised weight, and the weight
-// gradient from the quantised rows.
+// the FP8 product of quantised rows with a quantised weight, with or without an
+// epilogue, and the weight gradient from the quantised rows.
 #include <algorithm>
 #include <type_traits>
 
+#include "activation.h"
 #include "blockfmt.h"
 
 namespace {
@@ -175,6 +176,126 @@ __device__ __forceinline__ void store_columns(uint16_t* out, int col, int n, con
   }
 }
 
+// Four consecutive elements of a bf16 row, from `col` on; 0 past its end.
+__device__ __forceinline__ f32x4_t load_columns(const uint16_t* in, int col, int n) {
+  uint2 u = make_uint2(0, 0);
+  if (col + 4 <= n) {
+    __builtin_memcpy(&u, in + col, 8);
+  } else {
+    unsigned e[3];
+#pragma unroll
+    for (int c = 0; c < 3; ++c) e[c] = col + c < n ? in[col + c] : 0u;
+    u = make_uint2(e[0] | e[1] << 16, e[2]);
+  }
+  return f32x4_t{bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y)};
+}
+
+// What becomes of the sums a . b^T.  y as it is:
+struct PlainOut {
+  static constexpr bool kEpilogue = false;
+  uint16_t* y;
+};
+
+// fp32, for a kernel that goes on from there:
+struct SumsOut {
+  static constexpr bool kEpilogue = false;
+  float* sums;
+};
+
+// y = act(sum + bias) + residual.  A thread holds 8 columns, the same ones of
+// every row that it finishes.
+struct LinearOut {
+  static constexpr bool kEpilogue = true;
+  const uint16_t *bias, *residual;
+  int act;
+  uint16_t* y;
+  __device__ __forceinline__ uint4 ahead(int64_t row, int col, int n) const {
+    return residual != nullptr ? load_chunk<false>(residual + row * n, col, n) : make_uint4(0, 0, 0, 0);
+  }
+  template <int ACT>
+  __device__ __forceinline__ void finish(float (&v)[8], const float (&b)[8], const uint4 more, int64_t row, int col,
+                                         int n) const {
+    float r[8];
+    unpack8(more, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = activate<ACT>(v[j] + b[j]) + r[j];
+    store_chunk<false>(y + row * n, col, n, pack8(v));
+  }
+};
+
+// h = act(t), t = sum + bias, both in the block format: 16 lanes hold a block's
+// 8 columns each.
+struct BlocksOut {
+  static constexpr bool kEpilogue = true;
+  const uint16_t* bias;
+  int act;
+  uint8_t *hq, *hs, *cq, *cs;
+  int qcols, scols;                               // of a row
+  __device__ __forceinline__ uint4 ahead(int64_t, int, int) const { return make_uint4(0, 0, 0, 0); }
+  template <int ACT>
+  __device__ __forceinline__ void finish(float (&v)[8], const float (&b)[8], const uint4, int64_t row, int col,
+                                         int n) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = col + j < n ? v[j] + b[j] : 0.0f;
+    const int chunk = col / 8, chunks = qcols / 8, blocks = qcols / kBlock;
+    const bool last = chunk / kBlockChunks == blocks - 1;
+    if (cq != nullptr) {
+      quantize_chunk(v, cq + row * qcols, cs + row * scols, chunk, chunks);
+      if (last) pad_scales(cs + row * scols, blocks, scols, chunk % kBlockChunks);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = activate<ACT>(v[j]);
+    quantize_chunk(v, hq + row * qcols, hs + row * scols, chunk, chunks);
+    if (last) pad_scales(hs + row * scols, blocks, scols, chunk % kBlockChunks);
+  }
+};
+
+// Sums of COLS columns of a row in LDS, fp32: rows apart by a bank group, and the
+// second half's 16-byte pieces in swapped pairs, so that 16 lanes that read 8
+// columns each, and 16 that write 4 of a row each, spread over all banks.
+template <int COLS>
+struct SumRow {
+  static constexpr int kBytes = 4 * COLS + 16;
+  static __device__ __forceinline__ int at(int row, int piece) { return row * kBytes + 16 * (piece ^ (piece >> 4)); }
+  static __device__ __forceinline__ void load(const uint8_t* lds, int row, int c, float (&v)[8]) {      // columns 8 c..
+    const float4 a = *reinterpret_cast<const float4*>(lds + at(row, 2 * c));
+    const float4 b = *reinterpret_cast<const float4*>(lds + at(row, 2 * c + 1));
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+
+// ROWS rows of sums in LDS, finished by THREADS threads: thread t takes columns
+// col of rows t / (COLS / 8) and so on.  What a turn of U rows needs from memory
+// is loaded ahead of its arithmetic.  Rows from `left` on are not there.
+template <int COLS, int ROWS, int THREADS, typename Out>
+__device__ __forceinline__ void finish_rows(const Out& out, const uint8_t* lds, int thread, int row0, int left, int col0,
+                                            int n) {
+  constexpr int kPer = THREADS / (COLS / 8), kTurns = ROWS / kPer, U = kTurns < 4 ? kTurns : 4;
+  static_assert(THREADS % (COLS / 8) == 0 && ROWS % kPer == 0 && kTurns % U == 0, "whole turns");
+  const int c = thread % (COLS / 8), col = col0 + 8 * c, first = thread / (COLS / 8);
+  float bias[8] = {};
+  if (out.bias != nullptr) unpack8(load_chunk<false>(out.bias, col, n), bias);
+  with_activation(out.act, [&](auto act) {
+#pragma unroll 1
+    for (int i = 0; i < kTurns; i += U) {
+      uint4 more[U];
+      float v[U][8];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int row = first + (i + u) * kPer;
+        more[u] = out.ahead(row0 + min(row, left - 1), col, n);
+        SumRow<COLS>::load(lds, row, c, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int row = first + (i + u) * kPer;
+        if (row < left) out.template finish<act>(v[u], bias, more[u], row0 + row, col, n);
+      }
+    }
+  });
+}
+
 // The middle sizes: tiles of BN = 16 NT WN rows of b and BM = 16 MT WM rows of
 // a.  KG groups of WN x WM wavefronts share a tile and take the steps in turn,
 // which keeps a CU's memory pipeline busy where there are few tiles; their sums
@@ -200,13 +321,13 @@ struct MatmulTile {
   static constexpr int kSums = (KG - 1) * kGroup * NT * MT * 1024;                // at the end: the groups' sums,
   static constexpr int kRow = 2 * BN + 16;                                        // then rows of bf16, bank groups apart
   static_assert(kSums + BM * kRow <= kLds, "they fit where the operands were");
+  static_assert(kSums + BM * SumRow<BN>::kBytes <= kLds, "rows of fp32 too");
 };
 
-template <int NT, int MT, int WN, int WM, int KG, int S>
+template <int NT, int MT, int WN, int WM, int KG, int S, typename Out>
 __global__ __launch_bounds__(64 * WN * WM * KG) void matmul_tiles_kernel(
     const uint8_t* __restrict__ qa, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ qb,
-    const uint8_t* __restrict__ sb, int m, int n, int kcols, int kscales, uint16_t* __restrict__ y, int split_steps,
-    float* __restrict__ partial) {
+    const uint8_t* __restrict__ sb, int m, int n, int kcols, int kscales, const Out out, int split_steps) {
   using T = MatmulTile<NT, MT, WN, WM, KG, S>;
   __shared__ __align__(128) uint8_t lds[T::kLds];
   const int lane = threadIdx.x & 63;
@@ -306,20 +427,32 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void matmul_tiles_kernel(
         for (int i = 0; i < NT * MT; ++i) (&acc[0][0])[i] += sums[((q * T::kGroup + wave) * NT * MT + i) * 64 + lane];
     }
   }
-  if (partial != nullptr) {
+  if constexpr (std::is_same_v<Out, SumsOut>) {
     if (group > 0) return;
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
       const int row = m0 + 16 * (MT * wm + j) + r;
       if (row >= m) continue;
-      float* out = partial + (static_cast<int64_t>(blockIdx.y) * m + row) * n;
+      float* to = out.sums + (static_cast<int64_t>(blockIdx.y) * m + row) * n;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) store_sums(out, n0 + 16 * (NT * wn + i) + 4 * g, n, acc[i][j], false);
+      for (int i = 0; i < NT; ++i) store_sums(to, n0 + 16 * (NT * wn + i) + 4 * g, n, acc[i][j], false);
     }
     return;
   }
   // The tile goes through LDS, so that whole rows of it are stored.
   uint8_t* rows = lds + T::kSums;
+  if constexpr (Out::kEpilogue) {
+    if (group == 0) {
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          *reinterpret_cast<f32x4_t*>(rows + SumRow<T::BN>::at(16 * (MT * wm + j) + r, 4 * (NT * wn + i) + g)) = acc[i][j];
+    }
+    __syncthreads();
+    finish_rows<T::BN, T::BM, T::kThreads>(out, rows, threadIdx.x, m0, m - m0, n0, n);
+    return;
+  }
   if (group == 0) {
 #pragma unroll
     for (int j = 0; j < MT; ++j)
@@ -331,9 +464,10 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void matmul_tiles_kernel(
   __syncthreads();
   for (int p = threadIdx.x; p < T::BM * T::BN / 8; p += T::kThreads) {
     const int row = p / (T::BN / 8), c = p % (T::BN / 8);
-    if (m0 + row < m)
-      store_chunk<false>(y + static_cast<int64_t>(m0 + row) * n, n0 + 8 * c, n,
-                         *reinterpret_cast<const uint4*>(rows + row * T::kRow + 16 * c));
+    if constexpr (std::is_same_v<Out, PlainOut>)
+      if (m0 + row < m)
+        store_chunk<false>(out.y + static_cast<int64_t>(m0 + row) * n, n0 + 8 * c, n,
+                           *reinterpret_cast<const uint4*>(rows + row * T::kRow + 16 * c));
   }
 }
 
@@ -349,10 +483,10 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void matmul_tiles_kernel(
 // are in the last-level cache (3.1 TB/s; launch and the two latencies are
 // most of it), 1 x 14336 x 3584: 11.6 us (4.4 TB/s), 32 x 4096 x 4096: 10.0.
 constexpr int kFewWaves = 8;
-template <int MT>
+template <int MT, typename Out>
 __global__ __launch_bounds__(64 * kFewWaves) void matmul_few_kernel(
     const uint8_t* __restrict__ qa, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ qb,
-    const uint8_t* __restrict__ sb, int m, int n, int kcols, int kscales, uint16_t* __restrict__ y) {
+    const uint8_t* __restrict__ sb, int m, int n, int kcols, int kscales, const Out out) {
   constexpr int kAhead = 4;
   __shared__ __align__(16) f32x4_t part[kFewWaves][MT][64];
   const int lane = threadIdx.x & 63;
@@ -402,8 +536,21 @@ __global__ __launch_bounds__(64 * kFewWaves) void matmul_few_kernel(
     f32x4_t v = part[0][j][lane];
 #pragma unroll
     for (int w = 1; w < kFewWaves; ++w) v += part[w][j][lane];
-    const int row = 16 * j + r;
-    if (row < m) store_columns(y + static_cast<int64_t>(row) * n, n0 + 4 * g, n, v);
+    const int row = 16 * j + r, col = n0 + 4 * g;
+    if (row >= m) continue;
+    if constexpr (std::is_same_v<Out, SumsOut>) {
+      store_sums(out.sums + static_cast<int64_t>(row) * n, col, n, v, false);
+    } else {
+      if constexpr (std::is_same_v<Out, LinearOut>) {
+        if (out.bias != nullptr) v += load_columns(out.bias, col, n);
+        with_activation(out.act, [&](auto act) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) v[c] = activate<act>(v[c]);
+        });
+        if (out.residual != nullptr) v += load_columns(out.residual + static_cast<int64_t>(row) * n, col, n);
+      }
+      store_columns(out.y + static_cast<int64_t>(row) * n, col, n, v);
+    }
   }
 }
 
@@ -468,9 +615,10 @@ constexpr int kBig = 256;                       // rows of either operand in a t
 constexpr int kOperand = kBig * kBlock;         // bytes of a step
 constexpr int kScaleBuffer = 2048;              // a dword of scale bytes (four steps) for each row, twice over
 
+template <typename Out>
 __global__ __launch_bounds__(256) void matmul_large_kernel(
     const uint8_t* __restrict__ qa, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ qb,
-    const uint8_t* __restrict__ sb, int m, int n, int kcols, int kscales, uint16_t* __restrict__ y) {
+    const uint8_t* __restrict__ sb, int m, int n, int kcols, int kscales, const Out out) {
   constexpr int NT = 8, MT = 8;
   constexpr int NR = NT - 2;                       // b fragments read into the registers they were in
   __shared__ __align__(128) uint8_t lds[4 * kOperand + 2 * kScaleBuffer];      // a, a, b, b, scales
@@ -597,12 +745,30 @@ __global__ __launch_bounds__(256) void matmul_large_kernel(
   copies_left<0>();
   accumulators_done(acc);
   // 64 x 128 results of a wavefront at a time go through LDS, so that a store
-  // covers four whole rows of 256 bytes and not 16 pieces of 32.
+  // covers four whole rows of 256 bytes and not 16 pieces of 32, and an epilogue
+  // is a loop: written out over 256 accumulators it would be tens of kilobytes.
   constexpr int kRow = 256 + 16;                   // bytes, apart by a bank group
   __syncthreads();
   int thread = threadIdx.x;
   opaque(thread);                                  // not kept in registers over the loop
   const int er = thread & 15, eg = thread >> 4 & 3;
+  if constexpr (Out::kEpilogue) {
+    using Row = SumRow<kBlock>;
+    static_assert(4 * 64 * Row::kBytes <= sizeof(lds), "the four wavefronts' rows fit where the operands were");
+    uint8_t* sums = lds + wave * (64 * Row::kBytes);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4_t*>(sums + Row::at(16 * j + er, 4 * i + eg)) = acc[i][4 * h + j];
+      fence();
+      const int row = m0 + 128 * wm + 64 * h, col = n0 + 128 * wn;
+      if (row < m && col < n) finish_rows<kBlock, 64, 64>(out, sums, thread & 63, row, m - row, col, n);
+      fence();
+    }
+    return;
+  }
   uint8_t* mine = lds + wave * (64 * kRow);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -619,7 +785,8 @@ __global__ __launch_bounds__(256) void matmul_large_kernel(
     for (int i = 0; i < 16; ++i) {
       const int row = m0 + 128 * wm + 64 * h + 4 * i + eg;
       const uint4 v = *reinterpret_cast<const uint4*>(mine + (4 * i + eg) * kRow + 16 * er);
-      if (row < m) store_chunk<false>(y + static_cast<int64_t>(row) * n, n0 + 128 * wn + 8 * er, n, v);
+      if constexpr (std::is_same_v<Out, PlainOut>)
+        if (row < m) store_chunk<false>(out.y + static_cast<int64_t>(row) * n, n0 + 128 * wn + 8 * er, n, v);
     }
     fence();
   }
@@ -1274,29 +1441,68 @@ void launch_partial_sums(const float* partial, int64_t count, int splits, T* out
                      partial, count, splits, out, add);
 }
 
+// The end of a product whose sums lie in memory, from `splits` parts of k that
+// are added in order: a wavefront for each 512 columns of a row.
+template <typename Out>
+__global__ __launch_bounds__(256) void finish_sums_kernel(const float* __restrict__ sums, int64_t m, int n, int splits,
+                                                          int segments, const Out out) {
+  const int64_t job = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6), row = job / segments;
+  if (row >= m) return;
+  const int col = 8 * (64 * static_cast<int>(job - row * segments) + static_cast<int>(threadIdx.x & 63));
+  const uint4 more = out.ahead(row, col, n);
+  float bias[8] = {}, v[8] = {};
+  if (out.bias != nullptr) unpack8(load_chunk<false>(out.bias, col, n), bias);
+  const float* from = sums + row * n + col;
+  if (col + 8 <= n) {
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      float p[8];
+      __builtin_memcpy(p, from + s * m * n, 32);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += p[j];
+    }
+  } else {
+    for (int s = 0; s < splits; ++s)
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (col + j < n) v[j] += from[s * m * n + j];
+  }
+  with_activation(out.act, [&](auto act) { out.template finish<act>(v, bias, more, row, col, n); });
+}
+
 struct MatmulArgs {
   const uint8_t *qa, *sa, *qb, *sb;
   int m, n, kcols, kscales;
-  uint16_t* y;
   float* workspace;
 };
 
 int64_t tiles_of(int64_t m, int64_t n, int64_t bm, int64_t bn) { return (m + bm - 1) / bm * ((n + bn - 1) / bn); }
 
-template <int MT>
-void launch_few(const MatmulArgs& p, hipStream_t stream) {
-  hipLaunchKernelGGL(matmul_few_kernel<MT>, dim3((p.n + 15) / 16), dim3(64 * kFewWaves), 0, stream, p.qa, p.sa, p.qb,
-                     p.sb, p.m, p.n, p.kcols, p.kscales, p.y);
+template <int MT, typename Out>
+void launch_few(const MatmulArgs& p, const Out& out, hipStream_t stream) {
+  hipLaunchKernelGGL((matmul_few_kernel<MT, Out>), dim3((p.n + 15) / 16), dim3(64 * kFewWaves), 0, stream, p.qa, p.sa,
+                     p.qb, p.sb, p.m, p.n, p.kcols, p.kscales, out);
 }
 
 // splits workgroups to a tile, of split_steps steps (a multiple of four) each.
-template <int NT, int MT, int WN, int WM, int KG, int S>
-void launch_tiles(const MatmulArgs& p, hipStream_t stream, int splits = 1, int split_steps = 1 << 30) {
+template <int NT, int MT, int WN, int WM, int KG, int S, typename Out>
+void launch_tiles(const MatmulArgs& p, const Out& out, hipStream_t stream, int splits = 1, int split_steps = 1 << 30) {
   using T = MatmulTile<NT, MT, WN, WM, KG, S>;
-  hipLaunchKernelGGL((matmul_tiles_kernel<NT, MT, WN, WM, KG, S>),
+  hipLaunchKernelGGL((matmul_tiles_kernel<NT, MT, WN, WM, KG, S, Out>),
                      dim3(static_cast<unsigned>(tiles_of(p.m, p.n, T::BM, T::BN)), splits), dim3(T::kThreads), 0,
-                     stream, p.qa, p.sa, p.qb, p.sb, p.m, p.n, p.kcols, p.kscales, p.y, split_steps,
-                     splits > 1 ? p.workspace : nullptr);
+                     stream, p.qa, p.sa, p.qb, p.sb, p.m, p.n, p.kcols, p.kscales, out, split_steps);
+}
+
+template <typename Out>
+void launch_finish(const MatmulArgs& p, const Out& out, int splits, hipStream_t stream) {
+  if constexpr (std::is_same_v<Out, PlainOut>) {
+    launch_partial_sums(p.workspace, static_cast<int64_t>(p.m) * p.n, splits, out.y, 0, stream);
+  } else {
+    const int segments = static_cast<int>((fp8_cols(p.n) + 511) / 512);
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.m) * segments + 3) / 4);
+    hipLaunchKernelGGL(finish_sums_kernel<Out>, dim3(grid), dim3(256), 0, stream, p.workspace, static_cast<int64_t>(p.m),
+                       p.n, splits, segments, out);
+  }
 }
 
 // Workgroups to a tile of 64 x 64, and their steps: at least about sixteen, and
@@ -1318,9 +1524,10 @@ Splits matmul_splits(int64_t m, int64_t n, int64_t kcols) {
   return {static_cast<int>((steps + each - 1) / each), static_cast<int>(each)};
 }
 
-void launch_big(const MatmulArgs& p, hipStream_t stream) {
-  hipLaunchKernelGGL(matmul_large_kernel, dim3(static_cast<unsigned>(tiles_of(p.m, p.n, kBig, kBig))), dim3(256), 0,
-                     stream, p.qa, p.sa, p.qb, p.sb, p.m, p.n, p.kcols, p.kscales, p.y);
+template <typename Out>
+void launch_big(const MatmulArgs& p, const Out& out, hipStream_t stream) {
+  hipLaunchKernelGGL(matmul_large_kernel<Out>, dim3(static_cast<unsigned>(tiles_of(p.m, p.n, kBig, kBig))), dim3(256), 0,
+                     stream, p.qa, p.sa, p.qb, p.sb, p.m, p.n, p.kcols, p.kscales, out);
 }
 
 // Which kernel: by the number of tiles against the 256 CUs.  Measured (us):
@@ -1344,25 +1551,43 @@ void launch_big(const MatmulArgs& p, hipStream_t stream) {
 // a quarter where few columns meet a nearly empty last round.
 // Up to 32 rows the direct loads win (16 rows: 6.7 against 9.7, 32: 9.5 against
 // 10.1), and at 64 rows the tiles do (15.2 against 10.5).
-void launch_matmul(const MatmulArgs& p, hipStream_t stream) {
+//
+// Outputs in the block format need 128 columns in one workgroup: up to the 128 x
+// 128 tiles the sums go through the workspace instead, and a second kernel ends it.
+template <typename Out>
+void launch_matmul(const MatmulArgs& p, const Out& out, hipStream_t stream) {
+  constexpr bool kBlocks = std::is_same_v<Out, BlocksOut>;
   const int64_t t64 = tiles_of(p.m, p.n, 64, 64), t128 = tiles_of(p.m, p.n, 128, 128);
-  if (p.m <= 16)
-    launch_few<1>(p, stream);
-  else if (p.m <= 32)
-    launch_few<2>(p, stream);
-  else if (const Splits s = matmul_splits(p.m, p.n, p.kcols); s.count > 1) {
-    launch_tiles<2, 2, 2, 2, 2, 4>(p, stream, s.count, s.steps);
-    launch_partial_sums(p.workspace, static_cast<int64_t>(p.m) * p.n, s.count, p.y, 0, stream);
-  } else if (t64 <= 256)
-    launch_tiles<2, 2, 2, 2, 2, 4>(p, stream);
-  else if (t64 <= 768)
-    launch_tiles<2, 2, 2, 2, 1, 3>(p, stream);
-  else if (t128 <= 256)
-    launch_tiles<4, 4, 2, 2, 2, 2>(p, stream);
+  const Splits s = matmul_splits(p.m, p.n, p.kcols);
+  const auto small = [&](const auto& to) {
+    if (p.m <= 16)
+      launch_few<1>(p, to, stream);
+    else if (p.m <= 32)
+      launch_few<2>(p, to, stream);
+    else if (t64 <= 256)
+      launch_tiles<2, 2, 2, 2, 2, 4>(p, to, stream, s.count, s.steps);
+    else
+      launch_tiles<2, 2, 2, 2, 1, 3>(p, to, stream);
+  };
+  if (p.m <= 32 || t64 <= 768) {
+    if (kBlocks || s.count > 1) {
+      small(SumsOut{p.workspace});
+      launch_finish(p, out, s.count, stream);
+    } else if constexpr (!kBlocks) {
+      small(out);
+    }
+  } else if (t128 <= 256)
+    launch_tiles<4, 4, 2, 2, 2, 2>(p, out, stream);
   else if (t128 <= 512)
-    launch_tiles<4, 4, 2, 2, 1, 2>(p, stream);
+    launch_tiles<4, 4, 2, 2, 1, 2>(p, out, stream);
   else
-    launch_big(p, stream);
+    launch_big(p, out, stream);
+}
+
+// Bytes of sums in the workspace.
+size_t matmul_workspace(int64_t m, int64_t n, int64_t k, bool blocks) {
+  const int splits = matmul_splits(m, n, fp8_cols(k)).count;
+  return splits > 1 || (blocks && (m <= 32 || tiles_of(m, n, 64, 64) <= 768)) ? static_cast<size_t>(4 * m * n) * splits : 0;
 }
 
 template <int KT, int NT, int WK, int WN>
@@ -1457,8 +1682,7 @@ extern "C" {
 
 size_t taco_matmul_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   if (!matrix_ok(m, k) || !matrix_ok(n, k) || m > kMaxCodes / n) return 0;
-  const int splits = matmul_splits(m, n, fp8_cols(k)).count;
-  return splits > 1 ? static_cast<size_t>(4 * m * n) * splits : 0;
+  return matmul_workspace(m, n, k, false);
 }
 
 taco_status_t taco_matmul_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb, int64_t m,
@@ -1478,7 +1702,68 @@ taco_status_t taco_matmul_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_
                {qb, static_cast<size_t>(n * kcols)}, {sb, static_cast<size_t>((n + kBlock - 1) / kBlock * kscales)}}))
     return TACO_ERR_ALIAS;
   launch_matmul({qa, sa, qb, sb, static_cast<int>(m), static_cast<int>(n), static_cast<int>(kcols),
-                 static_cast<int>(kscales), static_cast<uint16_t*>(y_bf16), static_cast<float*>(workspace)}, stream);
+                 static_cast<int>(kscales), static_cast<float*>(workspace)},
+                PlainOut{static_cast<uint16_t*>(y_bf16)}, stream);
+  return launched();
+}
+
+size_t taco_linear_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k) { return taco_matmul_fp8_workspace_bytes(m, n, k); }
+
+taco_status_t taco_linear_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb,
+                              const void* bias_bf16, const void* residual_bf16, int32_t activation, int64_t m, int64_t n,
+                              int64_t k, void* y_bf16, void* workspace, size_t workspace_bytes, taco_stream_t stream) {
+  if (!qa || !sa || !qb || !sb || !y_bf16) return TACO_ERR_NULL;
+  if (!matrix_ok(m, k) || !matrix_ok(n, k) || m > kMaxCodes / n) return TACO_ERR_SHAPE;
+  if (!activation_ok(activation)) return TACO_ERR_FLAGS;
+  if (!aligned(qa, 16) || !aligned(qb, 16) || !aligned(y_bf16, 16) || !aligned(sa, 4) || !aligned(sb, 4) ||
+      !aligned(bias_bf16, 16) || !aligned(residual_bf16, 16) || !aligned(workspace, 256))
+    return TACO_ERR_ALIGN;
+  if (const size_t need = taco_linear_fp8_workspace_bytes(m, n, k);
+      need > 0 && (!workspace || workspace_bytes < need))
+    return TACO_ERR_WORKSPACE;
+  const int64_t kcols = fp8_cols(k), kscales = fp8_scale_cols(k);
+  const size_t size = static_cast<size_t>(2 * m * n);
+  if (aliased({{y_bf16, size}, {workspace, workspace_bytes}},
+              {{qa, static_cast<size_t>(m * kcols)}, {sa, static_cast<size_t>(m * kscales)},
+               {qb, static_cast<size_t>(n * kcols)}, {sb, static_cast<size_t>((n + kBlock - 1) / kBlock * kscales)},
+               {bias_bf16, static_cast<size_t>(2 * n)}, {residual_bf16, size}}))
+    return TACO_ERR_ALIAS;
+  launch_matmul({qa, sa, qb, sb, static_cast<int>(m), static_cast<int>(n), static_cast<int>(kcols),
+                 static_cast<int>(kscales), static_cast<float*>(workspace)},
+                LinearOut{static_cast<const uint16_t*>(bias_bf16), static_cast<const uint16_t*>(residual_bf16),
+                          activation, static_cast<uint16_t*>(y_bf16)}, stream);
+  return launched();
+}
+
+size_t taco_linear_quantize_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (!matrix_ok(m, k) || !matrix_ok(n, k) || !matrix_ok(m, n)) return 0;
+  return matmul_workspace(m, n, k, true);
+}
+
+taco_status_t taco_linear_quantize(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb,
+                                   const void* bias_bf16, int32_t activation, int64_t m, int64_t n, int64_t k,
+                                   uint8_t* hq, uint8_t* hs, uint8_t* cq, uint8_t* cs, void* workspace,
+                                   size_t workspace_bytes, taco_stream_t stream) {
+  if (!qa || !sa || !qb || !sb || !hq || !hs || (cq == nullptr) != (cs == nullptr)) return TACO_ERR_NULL;
+  if (!matrix_ok(m, k) || !matrix_ok(n, k) || !matrix_ok(m, n)) return TACO_ERR_SHAPE;
+  if (!activation_ok(activation)) return TACO_ERR_FLAGS;
+  if (!aligned(qa, 16) || !aligned(qb, 16) || !aligned(sa, 4) || !aligned(sb, 4) || !aligned(bias_bf16, 16) ||
+      !aligned(hq, 16) || !aligned(hs, 4) || !aligned(cq, 16) || !aligned(cs, 4) || !aligned(workspace, 256))
+    return TACO_ERR_ALIGN;
+  if (const size_t need = taco_linear_quantize_workspace_bytes(m, n, k);
+      need > 0 && (!workspace || workspace_bytes < need))
+    return TACO_ERR_WORKSPACE;
+  const int64_t kcols = fp8_cols(k), kscales = fp8_scale_cols(k), qcols = fp8_cols(n), scols = fp8_scale_cols(n);
+  if (aliased({{hq, static_cast<size_t>(m * qcols)}, {hs, static_cast<size_t>(m * scols)},
+               {cq, static_cast<size_t>(m * qcols)}, {cs, static_cast<size_t>(m * scols)}, {workspace, workspace_bytes}},
+              {{qa, static_cast<size_t>(m * kcols)}, {sa, static_cast<size_t>(m * kscales)},
+               {qb, static_cast<size_t>(n * kcols)}, {sb, static_cast<size_t>((n + kBlock - 1) / kBlock * kscales)},
+               {bias_bf16, static_cast<size_t>(2 * n)}}))
+    return TACO_ERR_ALIAS;
+  launch_matmul({qa, sa, qb, sb, static_cast<int>(m), static_cast<int>(n), static_cast<int>(kcols),
+                 static_cast<int>(kscales), static_cast<float*>(workspace)},
+                BlocksOut{static_cast<const uint16_t*>(bias_bf16), activation, hq, hs, cq, cs, static_cast<int>(qcols),
+                          static_cast<int>(scols)}, stream);
   return launched();
 }
 

@@ -1,8 +1,8 @@
 // Row-wise operators of the 8-bit linear layer (taco_linear.h) for gfx950:
 // quantisation, the norm with a residual and its gradient, the gated unit and
-// its gradient.  All of them are bound by HBM: each element is read once with
-// 16-byte loads, kept in registers between the row's reduction and its use,
-// and written once.
+// its gradient, the gradient of a nonlinearity and a bias.  All of them are
+// bound by HBM: each element is read once with 16-byte loads, kept in registers
+// between the row's reduction and its use, and written once.
 //
 // A lane holds chunks of 8 consecutive columns, 64 lanes 512 consecutive
 // columns, so a wavefront's loads cover 1 KiB and a block of 128 columns sits
@@ -14,6 +14,7 @@
 
 #include <algorithm>
 
+#include "activation.h"
 #include "blockfmt.h"
 
 namespace {
@@ -581,6 +582,75 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_any_kernel(
   }
 }
 
+// -------------------------------------------------------- nonlinearity, bias
+
+// dt = dh * act'(t), with its sums over rows.  A workgroup takes 512 columns of
+// `each` rows, a wavefront every fourth of them, kRowsAhead at a time so that
+// their loads are under way together; a lane keeps its 8 columns' sums in
+// registers, the wavefronts' are added in LDS in order, and the workgroup writes
+// one row of `sums` (dbias itself where there is but one group of rows).
+constexpr int kRowsAhead = 4;
+template <int ACT, bool WIDE>
+__global__ __launch_bounds__(kThreads) void activation_backward_kernel(
+    const uint16_t* __restrict__ dh, const uint8_t* __restrict__ cq, const uint8_t* __restrict__ cs, int64_t rows,
+    int cols, int segments, int each, uint16_t* __restrict__ dt, uint8_t* __restrict__ dq, uint8_t* __restrict__ ds,
+    float* __restrict__ sums, int64_t stride) {
+  __shared__ __align__(16) float part[kWaves][512];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t group = blockIdx.x / segments;
+  const int seg = static_cast<int>(blockIdx.x - group * segments);
+  const int64_t end = min(rows, (group + 1) * each);
+  const int64_t qcols = fp8_cols(cols), scols = fp8_scale_cols(cols);
+  const int chunks = static_cast<int>(qcols / 8), chunk = 64 * seg + lane, col = 8 * chunk;
+  float acc[8] = {};
+  for (int64_t row0 = group * each + wave; row0 < end; row0 += kWaves * kRowsAhead) {
+    uint4 d[kRowsAhead];
+    uint2 c[kRowsAhead];
+    unsigned byte[kRowsAhead];
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u) {
+      const int64_t row = min(row0 + kWaves * u, end - 1);
+      d[u] = load_chunk<WIDE>(dh + row * cols, col, cols);
+      c[u] = make_uint2(0, 0);
+      byte[u] = kScaleOne;
+      if (ACT != TACO_ACT_NONE && chunk < chunks) {
+        c[u] = *reinterpret_cast<const uint2*>(cq + row * qcols + col);
+        byte[u] = cs[row * scols + chunk / kBlockChunks];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u) {
+      const int64_t row = row0 + kWaves * u;
+      if (row >= end) continue;                     // the whole wavefront alike
+      float v[8];
+      unpack8(d[u], v);
+      if constexpr (ACT != TACO_ACT_NONE) {
+        float t[8];
+        decode8(c[u], scale_value(byte[u]), t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= slope<ACT>(t[j]);
+        store_chunk<WIDE>(dt + row * cols, col, cols, pack8(v));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] += v[j];
+      if (dq != nullptr) {
+        quantize_chunk(v, dq + row * qcols, ds + row * scols, chunk, chunks);
+        if (seg == segments - 1) pad_scales(ds + row * scols, chunks / kBlockChunks, static_cast<int>(scols), lane);
+      }
+    }
+  }
+  if (sums == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) part[wave][8 * lane + j] = acc[j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 512; i += kThreads) {
+    float v = part[0][i];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v += part[w][i];
+    if (512 * seg + i < cols) sums[group * stride + 512 * seg + i] = v;
+  }
+}
+
 // ------------------------------------------------------------------ launches
 
 constexpr int kRowChunks = 4;       // chunks per lane of quantize_rows
@@ -640,6 +710,49 @@ void launch_rmsnorm_backward_long(const NormGradient& p, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(backward_groups(p.rows, p.cols)), (p.cols + 8 * kThreads - 1) / (8 * kThreads));
   hipLaunchKernelGGL(rmsnorm_backward_long_kernel<WIDE>, grid, dim3(kThreads), 0, stream, p.dy, p.z, p.rstd, p.weight,
                      p.dz, p.rows, p.cols, p.means, p.dx, p.partial);
+}
+
+// Groups of rows of the nonlinearity's gradient: at least four rows each, a row
+// for each wavefront; no more than the column sums take in one turn, nor than
+// fill the CUs eight times.
+struct RowGroups {
+  int count, each;
+};
+RowGroups bias_groups(int64_t rows, int64_t cols) {
+  const int64_t segments = segments_of(fp8_cols(cols) / 8, 1);
+  const int64_t most = std::clamp<int64_t>(2048 / segments, 1, kSumClasses);
+  const int64_t least = rows <= 16 ? rows : (rows + most - 1) / most;
+  const int64_t each = (least + kWaves - 1) / kWaves * kWaves;
+  return {static_cast<int>((rows + each - 1) / each), static_cast<int>(each)};
+}
+
+struct ActivationGradient {
+  const uint16_t* dh;
+  const uint8_t *cq, *cs;
+  int64_t rows;
+  int cols;
+  uint16_t* dt;
+  uint8_t *dq, *ds;
+  float* dbias;
+  float* workspace;
+};
+
+template <int ACT>
+void launch_activation_backward(const ActivationGradient& p, hipStream_t stream) {
+  const RowGroups groups = bias_groups(p.rows, p.cols);
+  const int segments = segments_of(fp8_cols(p.cols) / 8, 1);
+  const int64_t stride = fp8_cols(p.cols);
+  float* sums = p.dbias == nullptr || groups.count == 1 ? p.dbias : p.workspace;
+  const dim3 grid(static_cast<unsigned>(groups.count) * segments), wg(kThreads);
+  if (p.cols % 8 == 0)
+    hipLaunchKernelGGL((activation_backward_kernel<ACT, true>), grid, wg, 0, stream, p.dh, p.cq, p.cs, p.rows, p.cols,
+                       segments, groups.each, p.dt, p.dq, p.ds, sums, stride);
+  else
+    hipLaunchKernelGGL((activation_backward_kernel<ACT, false>), grid, wg, 0, stream, p.dh, p.cq, p.cs, p.rows, p.cols,
+                       segments, groups.each, p.dt, p.dq, p.ds, sums, stride);
+  if (sums != p.dbias)
+    hipLaunchKernelGGL(column_sums_kernel, dim3(static_cast<unsigned>((p.cols + 15) / 16)), dim3(4 * kSumClasses), 0,
+                       stream, sums, groups.count, p.cols, stride, p.dbias);
 }
 
 constexpr int64_t kMaxNormCols = 65536;
@@ -810,6 +923,41 @@ taco_status_t taco_swiglu_backward(const void* dh_bf16, const uint8_t* cq, const
     hipLaunchKernelGGL(swiglu_backward_any_kernel, dim3(wave_grid(tokens, segments)), dim3(kThreads), 0, stream, dh,
                        cq, cs, tokens, static_cast<int>(inner), segments, dgu, dq, ds);
   }
+  return launched();
+}
+
+size_t taco_activation_backward_workspace_bytes(int64_t tokens, int64_t cols) {
+  if (!matrix_ok(tokens, cols)) return 0;
+  const int groups = bias_groups(tokens, cols).count;
+  return groups > 1 ? bytes(groups, fp8_cols(cols), 4) : 0;
+}
+
+taco_status_t taco_activation_backward(const void* dh_bf16, const uint8_t* cq, const uint8_t* cs, int32_t activation,
+                                       int64_t tokens, int64_t cols, void* dt_bf16, uint8_t* dq, uint8_t* ds,
+                                       float* dbias, void* workspace, size_t workspace_bytes, taco_stream_t stream) {
+  const bool none = activation == TACO_ACT_NONE;
+  if (!dh_bf16 || (cq == nullptr) != none || (cs == nullptr) != none || (dt_bf16 == nullptr) != none ||
+      (dq == nullptr) != (ds == nullptr) || (none && !dq && !dbias))
+    return TACO_ERR_NULL;
+  if (!matrix_ok(tokens, cols)) return TACO_ERR_SHAPE;
+  if (!activation_ok(activation)) return TACO_ERR_FLAGS;
+  if (!aligned(dh_bf16, 16) || !aligned(cq, 16) || !aligned(cs, 4) || !aligned(dt_bf16, 16) || !aligned(dq, 16) ||
+      !aligned(ds, 4) || !aligned(dbias, 4) || !aligned(workspace, 256))
+    return TACO_ERR_ALIGN;
+  if (const size_t need = taco_activation_backward_workspace_bytes(tokens, cols);
+      dbias && need > 0 && (!workspace || workspace_bytes < need))
+    return TACO_ERR_WORKSPACE;
+  const size_t n = bytes(tokens, cols, 2), codes = bytes(tokens, fp8_cols(cols)), scales = bytes(tokens, fp8_scale_cols(cols));
+  if (aliased({{dt_bf16, n}, {dq, codes}, {ds, scales}, {dbias, bytes(cols, 4)}, {workspace, workspace_bytes}},
+              {{dh_bf16, n}, {cq, codes}, {cs, scales}}))
+    return TACO_ERR_ALIAS;
+  const auto launch = activation == TACO_ACT_NONE ? launch_activation_backward<TACO_ACT_NONE>
+                    : activation == TACO_ACT_RELU ? launch_activation_backward<TACO_ACT_RELU>
+                    : activation == TACO_ACT_GELU ? launch_activation_backward<TACO_ACT_GELU>
+                    : activation == TACO_ACT_GELU_TANH ? launch_activation_backward<TACO_ACT_GELU_TANH>
+                                                       : launch_activation_backward<TACO_ACT_SILU>;
+  launch({static_cast<const uint16_t*>(dh_bf16), cq, cs, tokens, static_cast<int>(cols), static_cast<uint16_t*>(dt_bf16),
+          dq, ds, dbias, static_cast<float*>(workspace)}, stream);
   return launched();
 }
 

@@ -2,8 +2,9 @@
  * libtaco -- operators of an 8-bit linear layer for AMD Instinct MI355X
  * (gfx950): block-scaled FP8 quantisation, a root-mean-square norm with a
  * residual and a quantised output, the FP8 matrix product, the weight gradient
- * from an 8-bit checkpoint of the layer's input, and a SiLU-gated unit that
- * keeps its input in 8 bits.  Part of libtaco.so beside the compression calls
+ * from an 8-bit checkpoint of the layer's input, a SiLU-gated unit that
+ * keeps its input in 8 bits, and the product with a bias, a nonlinearity and a
+ * residual or an 8-bit output.  Part of libtaco.so beside the compression calls
  * of taco.h, whose conventions hold here too.
  *
  * Block format.  A matrix of `rows` rows and `cols` columns is held as
@@ -175,6 +176,77 @@ taco_status_t taco_swiglu_quantize(const void* gu_bf16, int64_t tokens, int64_t 
 taco_status_t taco_swiglu_backward(const void* dh_bf16, const uint8_t* cq, const uint8_t* cs,
                                    int64_t tokens, int64_t inner, void* dgu_bf16, uint8_t* dq,
                                    uint8_t* ds, taco_stream_t stream);
+
+/* Nonlinearities, t -> act(t):
+ *   TACO_ACT_NONE       t
+ *   TACO_ACT_RELU       max(t, 0)
+ *   TACO_ACT_GELU       t P(t), P the normal distribution function
+ *   TACO_ACT_GELU_TANH  t sigmoid(2 sqrt(2 / pi) (t + 0.044715 t^3))
+ *   TACO_ACT_SILU       t sigmoid(t)
+ * They are taken in fp32: with w the argument of the exponential in each (t^2 / 2,
+ * the sigmoid's, t), P and sigmoid have a relative error of at most
+ * (4 |w| + 24) 2^-24 where they are under a half, and the same absolutely above;
+ * values under 2^-100 may be 0.  A NaN stays one; at the infinities they take
+ * their limits. */
+enum {
+  TACO_ACT_NONE = 0,
+  TACO_ACT_RELU = 1,
+  TACO_ACT_GELU = 2,
+  TACO_ACT_GELU_TANH = 3,
+  TACO_ACT_SILU = 4
+};
+
+/*
+ * FP8 matrix product with its epilogue: y = bf16(act(a * b^T + bias) + residual).
+ * a, b and the sums as in taco_matmul_fp8; the rest is fp32, with one rounding at
+ * the end.
+ *   bias        bf16 [n]; may be NULL
+ *   residual    bf16 [m, n]; may be NULL
+ *   activation  TACO_ACT_*, anything else is TACO_ERR_FLAGS
+ *   y           out: bf16 [m, n]
+ */
+size_t taco_linear_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+taco_status_t taco_linear_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb,
+                              const uint8_t* sb, const void* bias_bf16, const void* residual_bf16,
+                              int32_t activation, int64_t m, int64_t n, int64_t k, void* y_bf16,
+                              void* workspace, size_t workspace_bytes, taco_stream_t stream);
+
+/*
+ * The same with quantised outputs, from fp32 (t is never stored otherwise):
+ *   t = a * b^T + bias,  h = act(t)
+ *   hq, hs  out: h [m, n] in the block format
+ *   cq, cs  out: t [m, n] in the block format, the checkpoint that
+ *           taco_activation_backward takes.  Both NULL: not kept.
+ * h and t within the limits above (TACO_ERR_SHAPE).
+ */
+size_t taco_linear_quantize_workspace_bytes(int64_t m, int64_t n, int64_t k);
+taco_status_t taco_linear_quantize(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb,
+                                   const uint8_t* sb, const void* bias_bf16, int32_t activation,
+                                   int64_t m, int64_t n, int64_t k, uint8_t* hq, uint8_t* hs,
+                                   uint8_t* cq, uint8_t* cs, void* workspace,
+                                   size_t workspace_bytes, taco_stream_t stream);
+
+/*
+ * Gradient of the nonlinearity and of the bias, at the checkpoint's values of t:
+ *   dt    = dh * act'(t)               (relu: 0 at t = 0; no nonlinearity: dh itself)
+ *   dbias = sum over tokens of dt      from dt before its rounding
+ *   dh      bf16 [tokens, cols]
+ *   cq, cs  t [tokens, cols] in the block format; NULL exactly for TACO_ACT_NONE
+ *   dt      out: bf16 [tokens, cols]; NULL for TACO_ACT_NONE
+ *   dq, ds  out: dt in the block format, from dt before its rounding to bf16.
+ *           Both NULL: not written.
+ *   dbias   out: fp32 [cols].  NULL: not written.
+ * For TACO_ACT_NONE one of dq and dbias at least (TACO_ERR_NULL).  act' has the
+ * error of its sigmoid or P, and of t times that and of its terms, absolutely:
+ * (4 w + 24) (1 + |t|) 2^-24 at most.  The workspace holds partial sums of dbias; it
+ * may be NULL where dbias is.
+ */
+size_t taco_activation_backward_workspace_bytes(int64_t tokens, int64_t cols);
+taco_status_t taco_activation_backward(const void* dh_bf16, const uint8_t* cq, const uint8_t* cs,
+                                       int32_t activation, int64_t tokens, int64_t cols,
+                                       void* dt_bf16, uint8_t* dq, uint8_t* ds, float* dbias,
+                                       void* workspace, size_t workspace_bytes,
+                                       taco_stream_t stream);
 
 #ifdef __cplusplus
 }

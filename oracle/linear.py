@@ -8,6 +8,8 @@ which is stored in bf16.  Test infrastructure: product code never imports it.
 """
 from __future__ import annotations
 
+import math
+
 import numpy as np
 
 from .taco_oracle import bf16_bits_to_f64, e4m3_decode, e4m3_encode, f64_to_bf16_bits
@@ -115,6 +117,57 @@ def swiglu(g: np.ndarray, u: np.ndarray) -> np.ndarray:
 def swiglu_backward(dh, g, u):
     s = sigmoid(g)
     return dh * u * s * (1.0 + g * (1.0 - s)), dh * g * s
+
+
+ACTIVATIONS = (None, "relu", "gelu", "gelu_tanh", "silu")
+
+
+def _normal(t: np.ndarray) -> np.ndarray:
+    """The normal distribution function; its tail from erfc, which does not cancel."""
+    return 0.5 * np.vectorize(math.erfc, otypes=[float])(-t / math.sqrt(2))
+
+
+def _tanh_argument(t: np.ndarray) -> np.ndarray:
+    return 2 * math.sqrt(2 / math.pi) * (t + 0.044715 * t ** 3)
+
+
+def activation(t: np.ndarray, name: str | None) -> np.ndarray:
+    """act(t); the limits at the infinities."""
+    with np.errstate(invalid="ignore", over="ignore"):
+        if name == "relu":
+            v = np.maximum(t, 0)
+        elif name == "gelu":
+            v = t * _normal(t)
+        elif name == "gelu_tanh":
+            v = t * sigmoid(_tanh_argument(t))
+        else:
+            v = t * sigmoid(t) if name == "silu" else t
+    return v if name is None else np.where(t == -np.inf, 0.0, v)
+
+
+def activation_slope(t: np.ndarray, name: str | None) -> np.ndarray:
+    """act'(t); 0 for relu at 0."""
+    if name is None:
+        return np.ones_like(t)
+    if name == "relu":
+        return np.where(np.isnan(t), t, (t > 0).astype(float))
+    if name == "gelu":
+        return _normal(t) + t * np.exp(-t * t / 2) / math.sqrt(2 * math.pi)
+    z, dz = (t, 1.0) if name == "silu" else (_tanh_argument(t), 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * t * t))
+    return sigmoid(z) + t * dz * sigmoid(z) * sigmoid(-z)
+
+
+def linear(a, b, bias=None, name=None, residual=None):
+    """(t, act(t) + residual), t = a b^T + bias."""
+    t = a @ b.T + (0 if bias is None else bias)
+    h = activation(t, name)
+    return t, h if residual is None else h + residual
+
+
+def activation_backward(dh, t, name):
+    """(dt, dbias)."""
+    dt = dh * activation_slope(t, name)
+    return dt, dt.sum(axis=0)
 
 
 def checkpoint(g: np.ndarray, u: np.ndarray):

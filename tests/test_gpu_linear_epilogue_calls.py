@@ -1,0 +1,174 @@
+"""How the product with an epilogue and the nonlinearity's gradient are called: workspaces, layouts, streams, graphs, and the
+three as a layer's forward and backward pass against differences of its own formula."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_compression_tensor_taco_amd as taco
+from oracle import linear as ol
+from test_gpu_linear import f64
+from test_gpu_linear_calls import activations, strided
+
+pytestmark = pytest.mark.gpu
+
+
+def layer(t, n, k, seed=0):
+    x, w = activations(t, k, seed), activations(n, k, seed + 1)
+    wq, ws, _, _ = taco.quantize_weight(w)
+    bias, residual, dh = activations(1, n, seed + 2)[0], activations(t, n, seed + 3), activations(t, n, seed + 4)
+    return taco.quantize_rows(x), (wq, ws), bias, residual, dh
+
+
+def same(got, want):
+    return all((a is None and b is None) or torch.equal(a, b) for a, b in zip(got, want))
+
+
+def calls(t, n, k):
+    """Every operator as (call, its tensor arguments)."""
+    (xq, xs), (wq, ws), bias, residual, dh = layer(t, n, k)
+    _, _, cq, cs = taco.linear_quantize(xq, xs, wq, ws, bias=bias, activation="gelu")
+    return [
+        (lambda a, b, c, d, e, f, **kw: (taco.linear_fp8(a, b, c, d, bias=e, activation="silu", residual=f, **kw),),
+         [xq, xs, wq, ws, bias, residual]),
+        (lambda a, b, c, d, e, **kw: taco.linear_quantize(a, b, c, d, bias=e, activation="gelu", **kw), [xq, xs, wq, ws, bias]),
+        (lambda a, b, c, **kw: taco.activation_backward(a, b, c, "gelu", **kw), [dh, cq, cs]),
+        (lambda a, **kw: taco.activation_backward(a, None, None, None, **kw)[1:], [dh]),
+    ]
+
+
+SHAPES = [(5, 300, 256), (200, 384, 640), (33, 77, 301), (600, 3001, 256)]
+
+
+@pytest.mark.parametrize("t,n,k", SHAPES)
+def test_strided_and_misaligned_arguments(t, n, k):
+    for call, given in calls(t, n, k):
+        want = call(*given)
+        for at in range(len(given)):
+            for view in strided(given[at]):
+                assert same(call(*given[:at], view, *given[at + 1:]), want)
+        for kind in range(2):
+            assert same(call(*(strided(a)[kind] for a in given)), want)
+
+
+def test_without_an_activation_dt_is_dh_itself():
+    dh = activations(9, 512, 0)
+    for view in (dh[:, :256], dh[:, ::2], dh):
+        assert taco.activation_backward(view, None, None, None)[0] is view
+
+
+@pytest.mark.parametrize("t,n,k", SHAPES)
+def test_another_stream(t, n, k):
+    stream = torch.cuda.Stream()
+    for call, given in calls(t, n, k):
+        want = call(*given)
+        views = [strided(a)[0] for a in given]
+        torch.cuda.synchronize()
+        plain, copied = call(*given, stream=stream), call(*views, stream=stream)
+        stream.synchronize()
+        assert same(plain, want) and same(copied, want)
+
+
+def test_workspaces_of_the_callers():
+    """Any contents, exactly the bytes that are named, and nothing beside them."""
+    (xq, xs), (wq, ws), bias, residual, dh = layer(300, 512, 8192)
+    cases = [(taco.linear_fp8_workspace_bytes(300, 512, 8192),
+              lambda w: (taco.linear_fp8(xq, xs, wq, ws, bias=bias, activation="relu", residual=residual, workspace=w),)),
+             (taco.linear_quantize_workspace_bytes(300, 512, 8192),
+              lambda w: taco.linear_quantize(xq, xs, wq, ws, bias=bias, activation="relu", workspace=w)),
+             (taco.linear_quantize_workspace_bytes(7, 512, 8192),
+              lambda w: taco.linear_quantize(xq[:7], xs[:7], wq, ws, bias=bias, activation="relu", workspace=w)),
+             (taco.activation_backward_workspace_bytes(300, 512),
+              lambda w: taco.activation_backward(dh, None, None, None, workspace=w))]
+    for need, call in cases:
+        assert need > 0
+        want = call(None)
+        whole = torch.full((need + 1024,), 0xFF, dtype=torch.uint8, device="cuda")      # NaN in every format
+        for workspace in (whole[512:512 + need], whole[256:]):
+            whole.fill_(0xFF)
+            assert same(call(workspace), want)
+            assert (whole[:256] == 0xFF).all() and (whole[512 + need:] == 0xFF).all()
+        for bad in (whole[512:511 + need], whole[513:513 + need]):
+            with pytest.raises(taco.TacoError):
+                call(bad)
+        for bad in (torch.zeros(2 * need, dtype=torch.uint8, device="cuda")[::2], torch.zeros(need, dtype=torch.uint8)):
+            with pytest.raises(ValueError):
+                call(bad)
+
+
+def test_refusals():
+    (xq, xs), (wq, ws), bias, residual, dh = layer(20, 300, 256)
+    q, s = taco.quantize_rows(dh)
+    bad = [lambda: taco.linear_fp8(xq, xs, wq[:, :128], ws), lambda: taco.linear_fp8(xq, xs[:, :2], wq, ws),
+           lambda: taco.linear_fp8(xq, xs, wq, ws, bias=bias[:-1]), lambda: taco.linear_fp8(xq, xs, wq, ws, bias=bias.float()),
+           lambda: taco.linear_fp8(xq, xs, wq, ws, residual=residual[:-1]),
+           lambda: taco.linear_fp8(xq, xs, wq, ws, residual=residual[0]), lambda: taco.linear_fp8(xq, xs, wq, ws, bias=bias.cpu()),
+           lambda: taco.linear_fp8(xq, xs, wq, ws, out=residual.float()),
+           lambda: taco.linear_quantize(xq, xs, wq, ws, activation="relu", checkpoint=False, cq=q),
+           lambda: taco.linear_quantize(xq, xs, wq, ws, cq=q, cs=s), lambda: taco.linear_quantize(xq, xs, wq, ws, hq=q[:, :128]),
+           lambda: taco.activation_backward(dh, None, None, "relu"), lambda: taco.activation_backward(dh, q, s, None),
+           lambda: taco.activation_backward(dh, q[:-1], s, "relu"), lambda: taco.activation_backward(dh, q, s[:, :1], "relu"),
+           lambda: taco.activation_backward(dh, None, None, None, dt=dh.clone()),
+           lambda: taco.activation_backward(dh, q, s, "relu", quantize=False, dq=q.clone()),
+           lambda: taco.activation_backward(dh, q, s, "relu", bias=False, dbias=torch.zeros(300).cuda())]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: taco.linear_fp8(xq, xs, wq, ws, residual=residual, out=residual),
+                 lambda: taco.activation_backward(dh, q, s, "relu", dt=dh), lambda: taco.activation_backward(dh, q, s, "relu", dq=q),
+                 lambda: taco.linear_quantize(xq, xs, wq, ws, hq=q, activation="relu", cq=q)):
+        with pytest.raises(taco.TacoError) as e:
+            call()
+        assert e.value.name == "TACO_ERR_ALIAS"
+    for call in (lambda: taco.activation_backward(dh, None, None, None, quantize=False, bias=False),):
+        with pytest.raises(taco.TacoError) as e:
+            call()
+        assert e.value.name == "TACO_ERR_NULL"
+
+
+def test_graph_with_eager_work_between_replays():
+    """Two layers and their gradients in one graph, with workspaces; replayed with new inputs."""
+    shapes = ((300, 512, 8192), (8, 640, 512), (700, 3001, 512))
+    given = [layer(*s) for s in shapes]
+
+    def step():
+        out = []
+        for (xq, xs), (wq, ws), bias, residual, dh in given:
+            hq, hs, cq, cs = taco.linear_quantize(xq, xs, wq, ws, bias=bias, activation="gelu")
+            out += [hq, hs, cq, cs, taco.linear_fp8(xq, xs, wq, ws, bias=bias, residual=residual)]
+            out += taco.activation_backward(dh, cq, cs, "gelu")
+        return out
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        held = step()
+    for replay in range(4):
+        for (t, n, k), ((xq, xs), _, bias, residual, dh) in zip(shapes, given):
+            q, s = taco.quantize_rows(activations(t, k, 100 + replay))
+            for to, v in ((xq, q), (xs, s), (bias, activations(1, n, 200 + replay)[0]), (residual, activations(t, n, 300 + replay)),
+                          (dh, activations(t, n, 400 + replay))):
+                to.copy_(v)
+        want = [v.clone() for v in step()]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(held, want), replay
+
+
+@pytest.mark.parametrize("name", ol.ACTIVATIONS[1:])
+def test_bias_gradient_against_differences(name):
+    """dbias is the derivative of sum(dh act(t)) along the bias at the checkpoint's t: the formula in fp64 there, by central
+    differences whose error is h^2 = 1e-10 of its third derivative and 1e-11 of rounding."""
+    (xq, xs), (wq, ws), bias, _, dh = layer(50, 200, 300)
+    _, _, cq, cs = taco.linear_quantize(xq, xs, wq, ws, bias=bias, activation=name)
+    dt, _, _, dbias = taco.activation_backward(dh, cq, cs, name)
+    t, g = ol.row_values(cq.cpu().numpy(), cs.cpu().numpy(), 200), f64(dh)
+    h = 1e-5
+    if name == "relu":
+        t = np.where(np.abs(t) <= h, t + 4 * h * np.sign(t) - (t == 0) * 4 * h, t)       # its slope has a step at 0
+    want = (g * (ol.activation(t + h, name) - ol.activation(t - h, name)) / (2 * h)).sum(0)
+    assert (np.abs(f64(dbias) - want) <= 1e-5 * np.abs(g).sum(0)).all()
+    assert (np.abs(f64(dt).sum(0) - want) <= 2.0 ** -8 * 1.13 * np.abs(g).sum(0) + 1e-5 * np.abs(g).sum(0)).all()
