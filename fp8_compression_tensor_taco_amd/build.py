@@ -1,4 +1,4 @@
-"""Build libtaco.so (HIP, gfx950) in-tree with hipcc, and the torch binding of its 8-bit linear layer.
+"""Build libtaco.so (HIP, gfx950) in-tree with hipcc, and the torch binding of its 8-bit linear layer and update.
 
 Usage: ``python -m fp8_compression_tensor_taco_amd.build`` or ``build_library()``.
 """
@@ -19,7 +19,9 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = [os.path.join(CSRC, "taco.hip")]                  # the compression calls (include/taco.h)
 LINEAR_SOURCES = [os.path.join(CSRC, "rowops.hip"),         # the 8-bit linear layer (include/taco_linear.h)
                   os.path.join(CSRC, "matmul.hip")]
-BINDING_SOURCE = os.path.join(CSRC, "linear_binding.cpp")   # host code only
+OPTIM_SOURCES = [os.path.join(CSRC, "optim.hip")]           # the update of a training step (include/taco_optim.h)
+BINDING_SOURCES = [os.path.join(CSRC, "linear_binding.cpp"),  # host code only
+                   os.path.join(CSRC, "optim_binding.cpp")]
 BINDING_PATH = os.path.join(PKG_DIR, "_linear_binding.so")
 ARCH = "gfx950"
 
@@ -54,7 +56,7 @@ def build_library(verbose: bool = True, binding_required: bool = False) -> str:
     warning says why, and an older one, which may not fit the new library, is
     removed; with ``binding_required`` the error is raised."""
     tmp = LIB_PATH + ".tmp"
-    cmd = [hipcc(), *compile_flags(), "-shared", "-parallel-jobs=3", *SOURCES, *LINEAR_SOURCES, "-o", tmp]
+    cmd = [hipcc(), *compile_flags(), "-shared", "-parallel-jobs=4", *SOURCES, *LINEAR_SOURCES, *OPTIM_SOURCES, "-o", tmp]
     _run(cmd, verbose)
     os.replace(tmp, LIB_PATH)
     try:
@@ -77,7 +79,7 @@ def build_binding(verbose: bool = True) -> str:
     tmp = BINDING_PATH + ".tmp"
     includes = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths()]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
-           *(f"-I{i}" for i in includes), BINDING_SOURCE, "-o", tmp, f"-L{PKG_DIR}", f"-l:{LIB_NAME}",
+           *(f"-I{i}" for i in includes), *BINDING_SOURCES, "-o", tmp, f"-L{PKG_DIR}", f"-l:{LIB_NAME}",
            "-Wl,-rpath,$ORIGIN", *(f"-L{i}" for i in cpp_extension.library_paths()), "-ltorch_python", "-ltorch_cpu",
            "-lc10"]
     _run(cmd, verbose)

@@ -5,98 +5,10 @@
 //
 // Every function takes the handle of the current stream last.  Tensors that are
 // not contiguous, or not 16-byte aligned, are copied.
-#include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <torch/csrc/utils/pybind.h>
-
-#include <optional>
-#include <string>
-#include <tuple>
-
+#include "binding.h"
 #include "taco_linear.h"
 
-namespace py = pybind11;
-
 namespace {
-
-using at::Tensor;
-using Given = std::optional<Tensor>;
-constexpr int64_t kBlock = 128;
-
-int64_t fp8_cols(int64_t cols) { return (cols + kBlock - 1) / kBlock * kBlock; }
-int64_t fp8_scale_cols(int64_t cols) { return (fp8_cols(cols) / kBlock + 3) / 4 * 4; }
-
-taco_stream_t stream_of(uint64_t handle) { return reinterpret_cast<taco_stream_t>(handle); }
-
-void check(taco_status_t status) {      // raises TacoError
-  if (status != TACO_OK)
-    py::module_::import("fp8_compression_tensor_taco_amd._binding").attr("_check")(static_cast<int>(status));
-}
-
-std::string text(at::IntArrayRef shape) {
-  std::string s = "(";
-  for (size_t i = 0; i < shape.size(); ++i) s += (i ? ", " : "") + std::to_string(shape[i]);
-  return s + (shape.size() == 1 ? ",)" : ")");
-}
-
-[[noreturn]] void refuse(const char* name, const std::string& what) {
-  throw py::value_error(std::string(name) + " must " + what);
-}
-
-const char* type_name(at::ScalarType t) {
-  return t == at::kBFloat16 ? "torch.bfloat16" : t == at::kFloat ? "torch.float32" : "torch.uint8";
-}
-
-// An input as the kernels take it.
-Tensor input(const Tensor& t, const char* name, at::ScalarType type, int64_t dims = 2) {
-  if (t.scalar_type() != type) refuse(name, std::string("be ") + type_name(type));
-  if (!t.is_cuda()) throw py::value_error("libtaco works on GPU tensors only (no CPU fallback)");
-  if (t.dim() != dims) refuse(name, "have " + std::to_string(dims) + " dimensions, got " + std::to_string(t.dim()));
-  if (!t.is_contiguous()) return t.contiguous();
-  return reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0 ? t : t.clone();
-}
-
-// The same, of a given shape and on the call's device.
-Tensor input(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape, at::Device device) {
-  Tensor c = input(t, name, type, static_cast<int64_t>(shape.size()));
-  if (c.sizes() != shape) refuse(name, "have shape " + text(shape) + ", got " + text(c.sizes()));
-  if (c.device() != device) throw py::value_error("all tensors must be on the same device");
-  return c;
-}
-
-Tensor output(const Given& t, const char* name, at::ScalarType type, at::IntArrayRef shape, at::Device device) {
-  if (!t) return at::empty(shape, at::TensorOptions(type).device(device));
-  if (t->scalar_type() != type || t->sizes() != shape || !t->is_contiguous() || t->device() != device)
-    refuse(name, std::string("be a contiguous ") + type_name(type) + " tensor of shape " + text(shape) + " on " +
-                     device.str());
-  return *t;
-}
-
-// The given workspace, or a new one per call: torch's allocator hands it out
-// again in the stream's order, and a captured graph keeps its own.
-struct Workspace {
-  Tensor held;
-  void* at = nullptr;
-  size_t bytes = 0;
-  Workspace(const Given& given, size_t need, at::Device device) {
-    if (given) {
-      if (!given->is_contiguous() || given->device() != device)
-        refuse("workspace", "be contiguous and on " + device.str());
-      held = *given;
-    } else if (need > 0) {
-      held = at::empty({static_cast<int64_t>(need)}, at::TensorOptions(at::kByte).device(device));
-    } else {
-      return;
-    }
-    at = held.data_ptr();
-    bytes = held.nbytes();
-  }
-};
-
-uint8_t* bytes_of(const Tensor& t) { return static_cast<uint8_t*>(t.data_ptr()); }
-float* floats_of(const Tensor& t) { return static_cast<float*>(t.data_ptr()); }
-py::object maybe(const Tensor& t) { return t.defined() ? py::cast(t) : py::none(); }
-uint8_t* maybe_bytes(const Tensor& t) { return t.defined() ? bytes_of(t) : nullptr; }
 
 std::tuple<Tensor, Tensor> quantize_rows(const Tensor& x_, const Given& q_, const Given& scale_, uint64_t stream) {
   const Tensor x = input(x_, "x", at::kBFloat16);
@@ -346,6 +258,8 @@ py::tuple activation_backward(const Tensor& dh_, const Given& cq_, const Given& 
 
 }  // namespace
 
+void define_optimizer(py::module_& m);             // optim_binding.cpp
+
 PYBIND11_MODULE(_linear_binding, m) {
   m.def("quantize_rows", &quantize_rows);
   m.def("quantize_weight", &quantize_weight);
@@ -358,4 +272,5 @@ PYBIND11_MODULE(_linear_binding, m) {
   m.def("linear_fp8", &linear_fp8);
   m.def("linear_quantize", &linear_quantize);
   m.def("activation_backward", &activation_backward);
+  define_optimizer(m);
 }
