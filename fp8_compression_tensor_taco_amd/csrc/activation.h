@@ -45,12 +45,12 @@ __device__ __forceinline__ float tanh_argument(float t) { return t * fmaf(t * t,
 
 template <int ACT>
 __device__ __forceinline__ float activate(float t) {
-  if constexpr (ACT == TACO_ACT_RELU) return t < 0.0f ? 0.0f : t;
+  if constexpr (ACT == TACO_ACT_RELU) return __builtin_elementwise_maximum(t, 0.0f);      // of a NaN: NaN
   if constexpr (ACT == TACO_ACT_GELU) {            // t P(t) = max(t, 0) - |t| P(-|t|)
     float tail, density;
     const float a = fminf(fabsf(t), 40.0f);
     normal_tail(a, tail, density);
-    return fmaf(-a, tail, t < 0.0f ? 0.0f : t);
+    return fmaf(-a, tail, __builtin_elementwise_maximum(t, 0.0f));
   }
   if constexpr (ACT == TACO_ACT_GELU_TANH) return fmaxf(t, -40.0f) * sigmoid2(tanh_argument(t));
   if constexpr (ACT == TACO_ACT_SILU) return fmaxf(t, -128.0f) * sigmoid2(kLog2E * t);

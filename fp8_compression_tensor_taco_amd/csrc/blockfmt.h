@@ -125,16 +125,18 @@ __device__ __forceinline__ unsigned scale_byte(unsigned amax_bits) {
 
 __device__ __forceinline__ unsigned abs_bits(float v) { return __builtin_bit_cast(unsigned, v) & 0x7FFFFFFFu; }
 
-// 8 codes of v * 2^(127 - byte); the product is exact, the conversion rounds
-// to nearest even.
+// 8 codes of v / 2^(byte - 127), rounded to nearest even; the conversion takes
+// the exponent of its fp32 scale, and the division is exact.
 __device__ __forceinline__ uint2 encode8(const float (&v)[8], unsigned byte) {
-  if (byte == kScaleNan) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  const float inv = __builtin_bit_cast(float, (254u - byte) << 23);
-  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, lo, true);
-  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, 0, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, hi, true);
-  return make_uint2(static_cast<unsigned>(lo), static_cast<unsigned>(hi));
+  typedef short i16x2_t __attribute__((ext_vector_type(2)));
+  const float s = __builtin_bit_cast(float, byte << 23);
+  i16x2_t lo = {0, 0}, hi = {0, 0};
+  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, v[0], v[1], s, false);
+  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, v[2], v[3], s, true);
+  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, v[4], v[5], s, false);
+  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, v[6], v[7], s, true);
+  const bool nan = byte == kScaleNan;
+  return make_uint2(nan ? 0x7F7F7F7Fu : __builtin_bit_cast(unsigned, lo), nan ? 0x7F7F7F7Fu : __builtin_bit_cast(unsigned, hi));
 }
 
 // 2^(byte - 127); NaN for 255.
@@ -152,15 +154,21 @@ __device__ __forceinline__ void decode8(const uint2 u, float s, float (&v)[8]) {
   v[4] = c[0] * s; v[5] = c[1] * s; v[6] = d[0] * s; v[7] = d[1] * s;
 }
 
+// Scale byte of the block that 16 lanes hold a chunk each of.  (A NaN stays one
+// in `maximum`, unlike in fmaxf.)
+__device__ __forceinline__ unsigned chunk_scale(const float (&v)[8]) {
+  float m = __builtin_fabsf(v[0]);
+#pragma unroll
+  for (int j = 1; j < 8; ++j) m = __builtin_elementwise_maximum(m, __builtin_fabsf(v[j]));
+  return scale_byte(block_max(abs_bits(m)));
+}
+
 // Quantises the chunk a lane holds of its block (all 16 lanes of the block
 // call this) and writes codes and, from the block's first lane, the scale byte.
 // q_row, scale_row: the row's codes and scale bytes; chunk: the lane's place.
 __device__ __forceinline__ void quantize_chunk(const float (&v)[8], uint8_t* q_row, uint8_t* scale_row, int chunk,
                                                int chunks) {
-  unsigned m = abs_bits(v[0]);
-#pragma unroll
-  for (int j = 1; j < 8; ++j) m = max(m, abs_bits(v[j]));
-  const unsigned byte = scale_byte(block_max(m));
+  const unsigned byte = chunk_scale(v);
   if (chunk < chunks) {
     *reinterpret_cast<uint2*>(q_row + 8 * static_cast<int64_t>(chunk)) = encode8(v, byte);
     if ((chunk & (kBlockChunks - 1)) == 0) scale_row[chunk / kBlockChunks] = static_cast<uint8_t>(byte);

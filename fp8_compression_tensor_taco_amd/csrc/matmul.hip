@@ -202,51 +202,85 @@ struct SumsOut {
   float* sums;
 };
 
-// y = act(sum + bias) + residual.  A thread holds 8 columns, the same ones of
-// every row that it finishes.
+// The epilogues.  A thread holds 8 columns, the same ones of every row that it
+// finishes, U rows at a time: those `apart` from each other from `row` on, as far
+// as `end`.  WHOLE: all of the tile's rows and columns are there, and rows are
+// 16-byte aligned; nothing branches then, so that the rows' chains of
+// instructions fill each other's gaps.
+
+// y = act(sum + bias) + residual.
 struct LinearOut {
   static constexpr bool kEpilogue = true;
   const uint16_t *bias, *residual;
   int act;
   uint16_t* y;
+  __device__ __forceinline__ bool whole_rows(int n) const { return n % 8 == 0; }
+  template <bool WHOLE>
   __device__ __forceinline__ uint4 ahead(int64_t row, int col, int n) const {
-    return residual != nullptr ? load_chunk<false>(residual + row * n, col, n) : make_uint4(0, 0, 0, 0);
+    return residual != nullptr ? load_chunk<WHOLE>(residual + row * n, col, n) : make_uint4(0, 0, 0, 0);
   }
-  template <int ACT>
-  __device__ __forceinline__ void finish(float (&v)[8], const float (&b)[8], const uint4 more, int64_t row, int col,
-                                         int n) const {
-    float r[8];
-    unpack8(more, r);
+  template <int ACT, bool WHOLE, int U>
+  __device__ __forceinline__ void finish(float (&v)[U][8], const float (&b)[8], const uint4 (&more)[U], int64_t row,
+                                         int apart, int64_t end, int col, int n) const {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = activate<ACT>(v[j] + b[j]) + r[j];
-    store_chunk<false>(y + row * n, col, n, pack8(v));
+    for (int u = 0; u < U; ++u) {
+      float r[8];
+      unpack8(more[u], r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[u][j] = activate<ACT>(v[u][j] + b[j]) + r[j];
+      if constexpr (WHOLE)
+        *reinterpret_cast<uint4*>(y + (row + u * apart) * n + col) = pack8(v[u]);
+      else if (row + u * apart < end)
+        store_chunk<false>(y + (row + u * apart) * n, col, n, pack8(v[u]));
+    }
   }
 };
 
 // h = act(t), t = sum + bias, both in the block format: 16 lanes hold a block's
-// 8 columns each.
+// 8 columns each.  The scale bytes of U rows are stored together, by a lane each.
 struct BlocksOut {
   static constexpr bool kEpilogue = true;
   const uint16_t* bias;
   int act;
   uint8_t *hq, *hs, *cq, *cs;
   int qcols, scols;                               // of a row
+  __device__ __forceinline__ bool whole_rows(int) const { return true; }
+  template <bool WHOLE>
   __device__ __forceinline__ uint4 ahead(int64_t, int, int) const { return make_uint4(0, 0, 0, 0); }
-  template <int ACT>
-  __device__ __forceinline__ void finish(float (&v)[8], const float (&b)[8], const uint4, int64_t row, int col,
-                                         int n) const {
+  template <bool WHOLE, int U>
+  __device__ __forceinline__ void quantize(const float (&v)[U][8], uint8_t* q, uint8_t* scale, int64_t row, int apart,
+                                           int64_t end, int col) const {
+    static_assert(U <= kBlockChunks, "a lane for each row");
+    const int lane = (col / 8) % kBlockChunks, block = col / kBlock;
+    unsigned mine = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = col + j < n ? v[j] + b[j] : 0.0f;
-    const int chunk = col / 8, chunks = qcols / 8, blocks = qcols / kBlock;
-    const bool last = chunk / kBlockChunks == blocks - 1;
-    if (cq != nullptr) {
-      quantize_chunk(v, cq + row * qcols, cs + row * scols, chunk, chunks);
-      if (last) pad_scales(cs + row * scols, blocks, scols, chunk % kBlockChunks);
+    for (int u = 0; u < U; ++u) {
+      const unsigned byte = chunk_scale(v[u]);
+      const uint2 codes = encode8(v[u], byte);
+      if (WHOLE || (row + u * apart < end && col < qcols))
+        *reinterpret_cast<uint2*>(q + (row + u * apart) * qcols + col) = codes;
+      mine = lane == u ? byte : mine;
     }
+    const int64_t at = row + lane * apart;
+    if (lane < U && (WHOLE || (at < end && col < qcols))) {
+      scale[at * scols + block] = static_cast<uint8_t>(mine);
+      if (block == qcols / kBlock - 1)
+        for (int i = block + 1; i < scols; ++i) scale[at * scols + i] = kScaleOne;
+    }
+  }
+  template <int ACT, bool WHOLE, int U>
+  __device__ __forceinline__ void finish(float (&v)[U][8], const float (&b)[8], const uint4 (&)[U], int64_t row, int apart,
+                                         int64_t end, int col, int n) const {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = activate<ACT>(v[j]);
-    quantize_chunk(v, hq + row * qcols, hs + row * scols, chunk, chunks);
-    if (last) pad_scales(hs + row * scols, blocks, scols, chunk % kBlockChunks);
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[u][j] = WHOLE || col + j < n ? v[u][j] + b[j] : 0.0f;
+    if (cq != nullptr) quantize<WHOLE>(v, cq, cs, row, apart, end, col);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[u][j] = activate<ACT>(v[u][j]);
+    quantize<WHOLE>(v, hq, hs, row, apart, end, col);
   }
 };
 
@@ -276,7 +310,7 @@ __device__ __forceinline__ void finish_rows(const Out& out, const uint8_t* lds, 
   const int c = thread % (COLS / 8), col = col0 + 8 * c, first = thread / (COLS / 8);
   float bias[8] = {};
   if (out.bias != nullptr) unpack8(load_chunk<false>(out.bias, col, n), bias);
-  with_activation(out.act, [&](auto act) {
+  const auto turns = [&](auto act, auto whole) {
 #pragma unroll 1
     for (int i = 0; i < kTurns; i += U) {
       uint4 more[U];
@@ -284,15 +318,16 @@ __device__ __forceinline__ void finish_rows(const Out& out, const uint8_t* lds, 
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int row = first + (i + u) * kPer;
-        more[u] = out.ahead(row0 + min(row, left - 1), col, n);
+        more[u] = out.template ahead<whole>(row0 + (whole ? row : min(row, left - 1)), col, n);
         SumRow<COLS>::load(lds, row, c, v[u]);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int row = first + (i + u) * kPer;
-        if (row < left) out.template finish<act>(v[u], bias, more[u], row0 + row, col, n);
-      }
+      out.template finish<act, whole>(v, bias, more, row0 + first + i * kPer, kPer, row0 + left, col, n);
     }
+  };
+  const bool whole = left >= ROWS && col0 + COLS <= n && out.whole_rows(n);
+  with_activation(out.act, [&](auto act) {
+    if (whole) turns(act, std::true_type{});
+    else turns(act, std::false_type{});
   });
 }
 
@@ -756,12 +791,16 @@ __global__ __launch_bounds__(256) void matmul_large_kernel(
     using Row = SumRow<kBlock>;
     static_assert(4 * 64 * Row::kBytes <= sizeof(lds), "the four wavefronts' rows fit where the operands were");
     uint8_t* sums = lds + wave * (64 * Row::kBytes);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    const auto hold = [&](auto first) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4_t*>(sums + Row::at(16 * j + er, 4 * i + eg)) = acc[i][4 * h + j];
+        for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4_t*>(sums + Row::at(16 * j + er, 4 * i + eg)) = acc[i][first + j];
+    };
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      if (h == 0) hold(std::integral_constant<int, 0>{});
+      else hold(std::integral_constant<int, 4>{});
       fence();
       const int row = m0 + 128 * wm + 64 * h, col = n0 + 128 * wn;
       if (row < m && col < n) finish_rows<kBlock, 64, 64>(out, sums, thread & 63, row, m - row, col, n);
@@ -1449,8 +1488,8 @@ __global__ __launch_bounds__(256) void finish_sums_kernel(const float* __restric
   const int64_t job = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6), row = job / segments;
   if (row >= m) return;
   const int col = 8 * (64 * static_cast<int>(job - row * segments) + static_cast<int>(threadIdx.x & 63));
-  const uint4 more = out.ahead(row, col, n);
-  float bias[8] = {}, v[8] = {};
+  const uint4 more[1] = {out.template ahead<false>(row, col, n)};
+  float bias[8] = {}, v[1][8] = {};
   if (out.bias != nullptr) unpack8(load_chunk<false>(out.bias, col, n), bias);
   const float* from = sums + row * n + col;
   if (col + 8 <= n) {
@@ -1459,15 +1498,15 @@ __global__ __launch_bounds__(256) void finish_sums_kernel(const float* __restric
       float p[8];
       __builtin_memcpy(p, from + s * m * n, 32);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += p[j];
+      for (int j = 0; j < 8; ++j) v[0][j] += p[j];
     }
   } else {
     for (int s = 0; s < splits; ++s)
 #pragma unroll
       for (int j = 0; j < 7; ++j)
-        if (col + j < n) v[j] += from[s * m * n + j];
+        if (col + j < n) v[0][j] += from[s * m * n + j];
   }
-  with_activation(out.act, [&](auto act) { out.template finish<act>(v, bias, more, row, col, n); });
+  with_activation(out.act, [&](auto act) { out.template finish<act, false>(v, bias, more, row, 1, m, col, n); });
 }
 
 struct MatmulArgs {

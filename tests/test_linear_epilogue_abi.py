@@ -2,6 +2,8 @@
 (CPU), all of which fail before any HIP call, so made-up pointers are never used; and the generated code of the large
 product's kernels, which write their matrix instructions as inline assembly."""
 import os
+import re
+import subprocess
 
 import pytest
 import torch
@@ -107,6 +109,15 @@ def test_binding_refusals():
         taco.linear_fp8(dh, s, q, s)
     with pytest.raises(ValueError, match="bfloat16"):
         taco.activation_backward(q, q, s, "relu")
+
+
+def test_no_scratch(tmp_path):
+    """No kernel keeps anything in scratch memory: accumulators there would be read and written around each instruction."""
+    for source in (s for s in build.LINEAR_SOURCES if s.endswith("matmul.hip")):
+        res = subprocess.run([build.hipcc(), *build.compile_flags(), "--cuda-device-only", "-S", source, "-o", str(tmp_path / "x.s"),
+                              "-Rpass-analysis=kernel-resource-usage"], capture_output=True, text=True, check=True)
+        sizes = re.findall(r"ScratchSize \[bytes/lane\]: (\d+)", res.stderr)
+        assert len(sizes) >= 10 and not any(int(n) for n in sizes)
 
 
 LARGE = [f"matmul_large_kernelINS_{kind}" for kind in ("9LinearOut", "9BlocksOut")]
