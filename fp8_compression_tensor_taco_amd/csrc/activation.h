@@ -20,61 +20,128 @@ __device__ __forceinline__ float over_one(float x) { return __builtin_amdgcn_rcp
 
 constexpr float kLog2E = 1.44269504f;
 
-// 1 / (1 + 2^-x); 2^-x may be infinite.
-__device__ __forceinline__ float sigmoid2(float x) { return over_one(1.0f + exp2_of(-x)); }
+// Values are taken some at a time, and each step of a formula for all of them
+// before the next: the steps of one value wait for each other, the hardware's
+// exponential and reciprocal longest, and the compiler left to itself puts one
+// value's behind another's (the scheduling barriers hold it off that).
+__device__ __forceinline__ void next_step() { __builtin_amdgcn_sched_barrier(0); }
 
-// The normal distribution function at -a, 0 <= a <= 40, and its density: a
-// polynomial in s = 1 / (1 + 0.31 a) times exp(-a^2 / 2), fitted so that the
-// largest relative error over a <= 14 is least: 1.6e-7, and under 6e-7 as it is
+// The normal distribution function at -a, 0 <= a <= 40, and exp(-a^2 / 2): a
+// polynomial in s = 1 / (1 + 0.31 a) times the latter, fitted so that the largest
+// relative error over a <= 14 is least: 1.6e-7, and under 6e-7 as it is
 // evaluated here, besides the exponential's.  Beyond 14 it is under 2^-146.
-__device__ __forceinline__ void normal_tail(float a, float& tail, float& density) {
-  const float s = over_one(fmaf(0.31f, a, 1.0f)), e = exp2_of(a * a * (-0.5f * kLog2E));
-  float p = fmaf(0.035841189f, s, -0.14160217f);
-  p = fmaf(p, s, 0.15506335f);
-  p = fmaf(p, s, -0.014898892f);
-  p = fmaf(p, s, 0.11010755f);
-  p = fmaf(p, s, 0.10777194f);
-  p = fmaf(p, s, 0.12406019f);
-  p = fmaf(p, s, 0.12365692f);
-  tail = p * s * e;
-  density = 0.39894228f * e;
+template <int N>
+__device__ __forceinline__ void normal_tail(const float (&a)[N], float (&tail)[N], float (&e)[N]) {
+  constexpr float kPoly[] = {0.035841189f, -0.14160217f, 0.15506335f, -0.014898892f,
+                             0.11010755f,  0.10777194f,  0.12406019f, 0.12365692f};
+  float s[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) s[j] = fmaf(0.31f, a[j], 1.0f);
+#pragma unroll
+  for (int j = 0; j < N; ++j) e[j] = a[j] * a[j];
+  next_step();
+#pragma unroll
+  for (int j = 0; j < N; ++j) s[j] = over_one(s[j]);
+#pragma unroll
+  for (int j = 0; j < N; ++j) e[j] *= -0.5f * kLog2E;
+  next_step();
+#pragma unroll
+  for (int j = 0; j < N; ++j) e[j] = exp2_of(e[j]);
+#pragma unroll
+  for (int j = 0; j < N; ++j) tail[j] = kPoly[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    next_step();
+#pragma unroll
+    for (int j = 0; j < N; ++j) tail[j] = fmaf(tail[j], s[j], kPoly[i]);
+  }
+  next_step();
+#pragma unroll
+  for (int j = 0; j < N; ++j) s[j] *= e[j];
+#pragma unroll
+  for (int j = 0; j < N; ++j) tail[j] *= s[j];
 }
 
 // 2 sqrt(2 / pi) (t + 0.044715 t^3) log2(e), so that (1 + tanh(..)) / 2 is its sigmoid2.
 __device__ __forceinline__ float tanh_argument(float t) { return t * fmaf(t * t, 0.10294324f, 2.3022082f); }
 
-template <int ACT>
-__device__ __forceinline__ float activate(float t) {
-  if constexpr (ACT == TACO_ACT_RELU) return __builtin_elementwise_maximum(t, 0.0f);      // of a NaN: NaN
-  if constexpr (ACT == TACO_ACT_GELU) {            // t P(t) = max(t, 0) - |t| P(-|t|)
-    float tail, density;
-    const float a = fminf(fabsf(t), 40.0f);
-    normal_tail(a, tail, density);
-    return fmaf(-a, tail, __builtin_elementwise_maximum(t, 0.0f));
-  }
-  if constexpr (ACT == TACO_ACT_GELU_TANH) return fmaxf(t, -40.0f) * sigmoid2(tanh_argument(t));
-  if constexpr (ACT == TACO_ACT_SILU) return fmaxf(t, -128.0f) * sigmoid2(kLog2E * t);
-  return t;
+// 1 / (1 + 2^-x); 2^-x may be infinite.
+template <int N>
+__device__ __forceinline__ void sigmoid2(const float (&x)[N], float (&s)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) s[j] = exp2_of(-x[j]);
+  next_step();
+#pragma unroll
+  for (int j = 0; j < N; ++j) s[j] += 1.0f;
+  next_step();
+#pragma unroll
+  for (int j = 0; j < N; ++j) s[j] = over_one(s[j]);
+  next_step();
 }
 
-template <int ACT>
-__device__ __forceinline__ float slope(float t) {
-  if constexpr (ACT == TACO_ACT_NONE) return 1.0f;
-  float v = t > 0.0f ? 1.0f : 0.0f;
-  if constexpr (ACT == TACO_ACT_GELU) {            // P(t) + t p(t)
-    float tail, density;
-    const float a = fminf(fabsf(t), 40.0f);
-    normal_tail(a, tail, density);
-    const float up = fmaf(a, density, -tail);      // P(a) + a p(a) - 1
-    v = t < 0.0f ? -up : 1.0f + up;
-  } else if constexpr (ACT == TACO_ACT_GELU_TANH) {
-    const float x = fminf(fmaxf(t, -40.0f), 40.0f), s = sigmoid2(tanh_argument(x));
-    v = s * fmaf(x * (1.0f - s), fmaf(x * x, 0.21406446f, 1.5957691f), 1.0f);
-  } else if constexpr (ACT == TACO_ACT_SILU) {
-    const float x = fminf(fmaxf(t, -128.0f), 128.0f), s = sigmoid2(kLog2E * x);
-    v = s * fmaf(x, 1.0f - s, 1.0f);
+// (`minimum` and `maximum` of a NaN are NaN, unlike fminf and fmaxf.)
+template <int ACT, int N>
+__device__ __forceinline__ void activate(float (&t)[N]) {
+  if constexpr (ACT == TACO_ACT_RELU) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) t[j] = __builtin_elementwise_maximum(t[j], 0.0f);
+  } else if constexpr (ACT == TACO_ACT_GELU) {     // t P(t) = max(t, 0) - |t| P(-|t|)
+    float a[N], tail[N], e[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) a[j] = __builtin_elementwise_minimum(__builtin_fabsf(t[j]), 40.0f);
+    normal_tail(a, tail, e);
+#pragma unroll
+    for (int j = 0; j < N; ++j) t[j] = fmaf(-a[j], tail[j], __builtin_elementwise_maximum(t[j], 0.0f));
+  } else if constexpr (ACT == TACO_ACT_GELU_TANH || ACT == TACO_ACT_SILU) {
+    constexpr float kLeast = ACT == TACO_ACT_SILU ? -128.0f : -40.0f;
+    float x[N], s[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = ACT == TACO_ACT_SILU ? kLog2E * t[j] : tanh_argument(t[j]);
+    sigmoid2(x, s);
+#pragma unroll
+    for (int j = 0; j < N; ++j) t[j] = __builtin_elementwise_maximum(t[j], kLeast) * s[j];
   }
-  return t != t ? t : v;
+}
+
+// t becomes the slope there.
+template <int ACT, int N>
+__device__ __forceinline__ void slope(float (&t)[N]) {
+  float v[N];
+  if constexpr (ACT == TACO_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) t[j] = 1.0f;
+  } else if constexpr (ACT == TACO_ACT_RELU) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = t[j] > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (ACT == TACO_ACT_GELU) {     // P(t) + t p(t)
+    float a[N], tail[N], e[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) a[j] = __builtin_elementwise_minimum(__builtin_fabsf(t[j]), 40.0f);
+    normal_tail(a, tail, e);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float up = fmaf(a[j] * 0.39894228f, e[j], -tail[j]);      // P(a) + a p(a) - 1
+      v[j] = t[j] < 0.0f ? -up : 1.0f + up;
+    }
+  } else {
+    constexpr float kMost = ACT == TACO_ACT_SILU ? 128.0f : 40.0f;
+    float x[N], z[N], s[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      x[j] = fminf(fmaxf(t[j], -kMost), kMost);
+      z[j] = ACT == TACO_ACT_SILU ? kLog2E * x[j] : tanh_argument(x[j]);
+    }
+    sigmoid2(z, s);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float steep = ACT == TACO_ACT_SILU ? 1.0f : fmaf(x[j] * x[j], 0.21406446f, 1.5957691f);
+      v[j] = s[j] * fmaf(x[j] * (1.0f - s[j]), steep, 1.0f);
+    }
+  }
+  if constexpr (ACT != TACO_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) t[j] = t[j] != t[j] ? t[j] : v[j];
+  }
 }
 
 // f(integral_constant) of the activation that a call names; uniform over the launch.

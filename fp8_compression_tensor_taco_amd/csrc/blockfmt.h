@@ -114,13 +114,12 @@ __device__ __forceinline__ unsigned block_max(unsigned m) {
 
 // Scale byte from the bits of a block's largest magnitude.  amax = m * 2^k with
 // 1 <= m < 2 and 448 = 1.75 * 2^8, so the exponent is k - 8, one more where m
-// exceeds 1.75.  Magnitudes are compared as integers: an infinity or a NaN
-// anywhere in the block wins and makes the byte NaN.
+// exceeds 1.75: a carry out of the mantissa.  Magnitudes are compared as
+// integers: an infinity or a NaN anywhere in the block wins and makes the byte NaN.
 __device__ __forceinline__ unsigned scale_byte(unsigned amax_bits) {
-  if (amax_bits >= 0x7F800000u) return kScaleNan;
-  if (amax_bits == 0) return kScaleOne;
-  const int e = static_cast<int>(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return static_cast<unsigned>(max(e, 1));
+  const int e = max(static_cast<int>((amax_bits + 0x1FFFFFu) >> 23) - 8, 1);
+  const unsigned byte = amax_bits == 0 ? kScaleOne : static_cast<unsigned>(e);
+  return amax_bits >= 0x7F800000u ? kScaleNan : byte;
 }
 
 __device__ __forceinline__ unsigned abs_bits(float v) { return __builtin_bit_cast(unsigned, v) & 0x7FFFFFFFu; }
@@ -154,13 +153,25 @@ __device__ __forceinline__ void decode8(const uint2 u, float s, float (&v)[8]) {
   v[4] = c[0] * s; v[5] = c[1] * s; v[6] = d[0] * s; v[7] = d[1] * s;
 }
 
-// Scale byte of the block that 16 lanes hold a chunk each of.  (A NaN stays one
-// in `maximum`, unlike in fmaxf.)
-__device__ __forceinline__ unsigned chunk_scale(const float (&v)[8]) {
-  float m = __builtin_fabsf(v[0]);
+// Scale bytes of U blocks, of each of which 16 lanes hold a chunk.  (A NaN stays
+// one in `maximum`, unlike in fmaxf.)
+template <int U>
+__device__ __forceinline__ void chunk_scales(const float (&v)[U][8], unsigned (&byte)[U]) {
 #pragma unroll
-  for (int j = 1; j < 8; ++j) m = __builtin_elementwise_maximum(m, __builtin_fabsf(v[j]));
-  return scale_byte(block_max(abs_bits(m)));
+  for (int u = 0; u < U; ++u) {
+    float m = __builtin_fabsf(v[u][0]);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) m = __builtin_elementwise_maximum(m, __builtin_fabsf(v[u][j]));
+    byte[u] = abs_bits(m);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) byte[u] = max(byte[u], row_rotated<0x128>(byte[u]));
+#pragma unroll
+  for (int u = 0; u < U; ++u) byte[u] = max(byte[u], row_rotated<0x124>(byte[u]));
+#pragma unroll
+  for (int u = 0; u < U; ++u) byte[u] = max(byte[u], row_rotated<0x122>(byte[u]));
+#pragma unroll
+  for (int u = 0; u < U; ++u) byte[u] = scale_byte(max(byte[u], row_rotated<0x121>(byte[u])));
 }
 
 // Quantises the chunk a lane holds of its block (all 16 lanes of the block
@@ -168,7 +179,10 @@ __device__ __forceinline__ unsigned chunk_scale(const float (&v)[8]) {
 // q_row, scale_row: the row's codes and scale bytes; chunk: the lane's place.
 __device__ __forceinline__ void quantize_chunk(const float (&v)[8], uint8_t* q_row, uint8_t* scale_row, int chunk,
                                                int chunks) {
-  const unsigned byte = chunk_scale(v);
+  const float one[1][8] = {{v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]}};
+  unsigned bytes[1];
+  chunk_scales(one, bytes);
+  const unsigned byte = bytes[0];
   if (chunk < chunks) {
     *reinterpret_cast<uint2*>(q_row + 8 * static_cast<int64_t>(chunk)) = encode8(v, byte);
     if ((chunk & (kBlockChunks - 1)) == 0) scale_row[chunk / kBlockChunks] = static_cast<uint8_t>(byte);

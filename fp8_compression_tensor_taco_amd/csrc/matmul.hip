@@ -203,10 +203,11 @@ struct SumsOut {
 };
 
 // The epilogues.  A thread holds 8 columns, the same ones of every row that it
-// finishes, U rows at a time: those `apart` from each other from `row` on, as far
-// as `end`.  WHOLE: all of the tile's rows and columns are there, and rows are
-// 16-byte aligned; nothing branches then, so that the rows' chains of
-// instructions fill each other's gaps.
+// finishes, U rows at a time: those `apart` from each other from `row` on, counted
+// from the tile's first row (row0, the same for all threads, so that a lane's
+// offset from there has 32 bits), of which `left` are there.  WHOLE: all of the
+// tile's rows and columns are there, and rows are 16-byte aligned; nothing branches
+// then, so that the rows' chains of instructions fill each other's gaps.
 
 // y = act(sum + bias) + residual.
 struct LinearOut {
@@ -215,23 +216,34 @@ struct LinearOut {
   int act;
   uint16_t* y;
   __device__ __forceinline__ bool whole_rows(int n) const { return n % 8 == 0; }
-  template <bool WHOLE>
-  __device__ __forceinline__ uint4 ahead(int64_t row, int col, int n) const {
-    return residual != nullptr ? load_chunk<WHOLE>(residual + row * n, col, n) : make_uint4(0, 0, 0, 0);
+  template <bool WHOLE, int U>
+  __device__ __forceinline__ void ahead(uint4 (&more)[U], int64_t row0, int row, int apart, int left, int col, int n) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      more[u] = make_uint4(0, 0, 0, 0);
+      if (residual == nullptr) continue;
+      if constexpr (WHOLE)
+        more[u] = *reinterpret_cast<const uint4*>(residual + (row0 + u * apart) * n + static_cast<unsigned>(row * n + col));
+      else
+        more[u] = load_chunk<false>(residual + (row0 + min(row + u * apart, left - 1)) * n, col, n);
+    }
   }
   template <int ACT, bool WHOLE, int U>
-  __device__ __forceinline__ void finish(float (&v)[U][8], const float (&b)[8], const uint4 (&more)[U], int64_t row,
-                                         int apart, int64_t end, int col, int n) const {
+  __device__ __forceinline__ void finish(float (&v)[U][8], const float (&b)[8], const uint4 (&more)[U], int64_t row0,
+                                         int row, int apart, int left, int col, int n) const {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float r[8];
       unpack8(more[u], r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[u][j] = activate<ACT>(v[u][j] + b[j]) + r[j];
+      for (int j = 0; j < 8; ++j) v[u][j] += b[j];
+      activate<ACT>(v[u]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[u][j] += r[j];
       if constexpr (WHOLE)
-        *reinterpret_cast<uint4*>(y + (row + u * apart) * n + col) = pack8(v[u]);
-      else if (row + u * apart < end)
-        store_chunk<false>(y + (row + u * apart) * n, col, n, pack8(v[u]));
+        *reinterpret_cast<uint4*>(y + (row0 + u * apart) * n + static_cast<unsigned>(row * n + col)) = pack8(v[u]);
+      else if (row + u * apart < left)
+        store_chunk<false>(y + (row0 + row + u * apart) * n, col, n, pack8(v[u]));
     }
   }
 };
@@ -245,42 +257,45 @@ struct BlocksOut {
   uint8_t *hq, *hs, *cq, *cs;
   int qcols, scols;                               // of a row
   __device__ __forceinline__ bool whole_rows(int) const { return true; }
-  template <bool WHOLE>
-  __device__ __forceinline__ uint4 ahead(int64_t, int, int) const { return make_uint4(0, 0, 0, 0); }
   template <bool WHOLE, int U>
-  __device__ __forceinline__ void quantize(const float (&v)[U][8], uint8_t* q, uint8_t* scale, int64_t row, int apart,
-                                           int64_t end, int col) const {
+  __device__ __forceinline__ void ahead(uint4 (&)[U], int64_t, int, int, int, int, int) const {}
+  template <bool WHOLE, int U>
+  __device__ __forceinline__ void quantize(const float (&v)[U][8], uint8_t* q, uint8_t* scale, int64_t row0, int row,
+                                           int apart, int left, int col) const {
     static_assert(U <= kBlockChunks, "a lane for each row");
     const int lane = (col / 8) % kBlockChunks, block = col / kBlock;
-    unsigned mine = 0;
+    const unsigned off = static_cast<unsigned>(row * qcols + col);
+    unsigned byte[U], mine = 0;
+    chunk_scales(v, byte);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const unsigned byte = chunk_scale(v[u]);
-      const uint2 codes = encode8(v[u], byte);
-      if (WHOLE || (row + u * apart < end && col < qcols))
-        *reinterpret_cast<uint2*>(q + (row + u * apart) * qcols + col) = codes;
-      mine = lane == u ? byte : mine;
+      const uint2 codes = encode8(v[u], byte[u]);
+      if (WHOLE || (row + u * apart < left && col < qcols))
+        *reinterpret_cast<uint2*>(q + (row0 + u * apart) * qcols + off) = codes;
+      mine = lane == u ? byte[u] : mine;
     }
-    const int64_t at = row + lane * apart;
-    if (lane < U && (WHOLE || (at < end && col < qcols))) {
-      scale[at * scols + block] = static_cast<uint8_t>(mine);
-      if (block == qcols / kBlock - 1)
-        for (int i = block + 1; i < scols; ++i) scale[at * scols + i] = kScaleOne;
+    const int at = row + lane * apart;
+    if (lane < U && (WHOLE || (at < left && col < qcols))) {
+      uint8_t* to = scale + row0 * scols + static_cast<unsigned>(at * scols);
+      to[block] = static_cast<uint8_t>(mine);
+      if (block == qcols / kBlock - 1) {
+#pragma unroll
+        for (int i = 1; i < 4; ++i)
+          if (block + i < scols) to[block + i] = kScaleOne;
+      }
     }
   }
   template <int ACT, bool WHOLE, int U>
-  __device__ __forceinline__ void finish(float (&v)[U][8], const float (&b)[8], const uint4 (&)[U], int64_t row, int apart,
-                                         int64_t end, int col, int n) const {
+  __device__ __forceinline__ void finish(float (&v)[U][8], const float (&b)[8], const uint4 (&)[U], int64_t row0, int row,
+                                         int apart, int left, int col, int n) const {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[u][j] = WHOLE || col + j < n ? v[u][j] + b[j] : 0.0f;
-    if (cq != nullptr) quantize<WHOLE>(v, cq, cs, row, apart, end, col);
+    if (cq != nullptr) quantize<WHOLE>(v, cq, cs, row0, row, apart, left, col);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[u][j] = activate<ACT>(v[u][j]);
-    quantize<WHOLE>(v, hq, hs, row, apart, end, col);
+    for (int u = 0; u < U; ++u) activate<ACT>(v[u]);
+    quantize<WHOLE>(v, hq, hs, row0, row, apart, left, col);
   }
 };
 
@@ -315,13 +330,11 @@ __device__ __forceinline__ void finish_rows(const Out& out, const uint8_t* lds, 
     for (int i = 0; i < kTurns; i += U) {
       uint4 more[U];
       float v[U][8];
+      const int row = first + i * kPer;
+      out.template ahead<whole>(more, row0, row, kPer, left, col, n);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int row = first + (i + u) * kPer;
-        more[u] = out.template ahead<whole>(row0 + (whole ? row : min(row, left - 1)), col, n);
-        SumRow<COLS>::load(lds, row, c, v[u]);
-      }
-      out.template finish<act, whole>(v, bias, more, row0 + first + i * kPer, kPer, row0 + left, col, n);
+      for (int u = 0; u < U; ++u) SumRow<COLS>::load(lds, row + u * kPer, c, v[u]);
+      out.template finish<act, whole>(v, bias, more, row0, row, kPer, left, col, n);
     }
   };
   const bool whole = left >= ROWS && col0 + COLS <= n && out.whole_rows(n);
@@ -578,10 +591,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void matmul_few_kernel(
     } else {
       if constexpr (std::is_same_v<Out, LinearOut>) {
         if (out.bias != nullptr) v += load_columns(out.bias, col, n);
-        with_activation(out.act, [&](auto act) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) v[c] = activate<act>(v[c]);
-        });
+        float t[4] = {v[0], v[1], v[2], v[3]};
+        with_activation(out.act, [&](auto act) { activate<act>(t); });
+        v = f32x4_t{t[0], t[1], t[2], t[3]};
         if (out.residual != nullptr) v += load_columns(out.residual + static_cast<int64_t>(row) * n, col, n);
       }
       store_columns(out.y + static_cast<int64_t>(row) * n, col, n, v);
@@ -1488,7 +1500,8 @@ __global__ __launch_bounds__(256) void finish_sums_kernel(const float* __restric
   const int64_t job = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6), row = job / segments;
   if (row >= m) return;
   const int col = 8 * (64 * static_cast<int>(job - row * segments) + static_cast<int>(threadIdx.x & 63));
-  const uint4 more[1] = {out.template ahead<false>(row, col, n)};
+  uint4 more[1] = {};
+  out.template ahead<false>(more, row, 0, 1, 1, col, n);
   float bias[8] = {}, v[1][8] = {};
   if (out.bias != nullptr) unpack8(load_chunk<false>(out.bias, col, n), bias);
   const float* from = sums + row * n + col;
@@ -1506,7 +1519,7 @@ __global__ __launch_bounds__(256) void finish_sums_kernel(const float* __restric
       for (int j = 0; j < 7; ++j)
         if (col + j < n) v[0][j] += from[s * m * n + j];
   }
-  with_activation(out.act, [&](auto act) { out.template finish<act, false>(v, bias, more, row, 1, m, col, n); });
+  with_activation(out.act, [&](auto act) { out.template finish<act, false>(v, bias, more, row, 0, 1, 1, col, n); });
 }
 
 struct MatmulArgs {

@@ -627,8 +627,9 @@ __global__ __launch_bounds__(kThreads) void activation_backward_kernel(
       if constexpr (ACT != TACO_ACT_NONE) {
         float t[8];
         decode8(c[u], scale_value(byte[u]), t);
+        slope<ACT>(t);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= slope<ACT>(t[j]);
+        for (int j = 0; j < 8; ++j) v[j] *= t[j];
         store_chunk<WIDE>(dt + row * cols, col, cols, pack8(v));
       }
 #pragma unroll
