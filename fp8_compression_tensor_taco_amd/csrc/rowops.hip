@@ -589,8 +589,15 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_any_kernel(
 // their loads are under way together; a lane keeps its 8 columns' sums in
 // registers, the wavefronts' are added in LDS in order, and the workgroup writes
 // one row of `sums` (dbias itself where there is but one group of rows).
+//
+// The loads have no branch, so that the compiler can count them and waits for one
+// row while the next ones' are under way: lanes past the end of a row load its last
+// chunk and drop it.  (Under a condition each was waited for where it stood:
+// 1021 x 1601 8.7 us.)  ROWS: rows of whole 16-byte pieces, of any length from 8, or
+// shorter ones.
+enum ActRows { kActWhole, kActOdd, kActShort };
 constexpr int kRowsAhead = 4;
-template <int ACT, bool WIDE>
+template <int ACT, ActRows ROWS>
 __global__ __launch_bounds__(kThreads) void activation_backward_kernel(
     const uint16_t* __restrict__ dh, const uint8_t* __restrict__ cq, const uint8_t* __restrict__ cs, int64_t rows,
     int cols, int segments, int each, uint16_t* __restrict__ dt, uint8_t* __restrict__ dq, uint8_t* __restrict__ ds,
@@ -602,6 +609,7 @@ __global__ __launch_bounds__(kThreads) void activation_backward_kernel(
   const int64_t end = min(rows, (group + 1) * each);
   const int64_t qcols = fp8_cols(cols), scols = fp8_scale_cols(cols);
   const int chunks = static_cast<int>(qcols / 8), chunk = 64 * seg + lane, col = 8 * chunk;
+  const int from = ROWS == kActShort ? 0 : min(col, cols - 8), held = min(chunk, chunks - 1);
   float acc[8] = {};
   for (int64_t row0 = group * each + wave; row0 < end; row0 += kWaves * kRowsAhead) {
     uint4 d[kRowsAhead];
@@ -610,27 +618,32 @@ __global__ __launch_bounds__(kThreads) void activation_backward_kernel(
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
       const int64_t row = min(row0 + kWaves * u, end - 1);
-      d[u] = load_chunk<WIDE>(dh + row * cols, col, cols);
-      c[u] = make_uint2(0, 0);
-      byte[u] = kScaleOne;
-      if (ACT != TACO_ACT_NONE && chunk < chunks) {
-        c[u] = *reinterpret_cast<const uint2*>(cq + row * qcols + col);
-        byte[u] = cs[row * scols + chunk / kBlockChunks];
+      if constexpr (ROWS == kActWhole)
+        d[u] = *reinterpret_cast<const uint4*>(dh + row * cols + from);
+      else if constexpr (ROWS == kActOdd)
+        __builtin_memcpy(&d[u], dh + row * cols + from, 16);
+      else
+        d[u] = load_chunk<false>(dh + row * cols, col, cols);
+      if constexpr (ACT != TACO_ACT_NONE) {
+        c[u] = *reinterpret_cast<const uint2*>(cq + row * qcols + 8 * held);
+        byte[u] = cs[row * scols + held / kBlockChunks];
       }
     }
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
       const int64_t row = row0 + kWaves * u;
       if (row >= end) continue;                     // the whole wavefront alike
+      if constexpr (ROWS == kActOdd) d[u] = drop_elements(d[u], min(col - from, 7));
+      const unsigned keep = col < cols ? ~0u : 0u;
       float v[8];
-      unpack8(d[u], v);
+      unpack8(make_uint4(d[u].x & keep, d[u].y & keep, d[u].z & keep, d[u].w & keep), v);
       if constexpr (ACT != TACO_ACT_NONE) {
         float t[8];
         decode8(c[u], scale_value(byte[u]), t);
         slope<ACT>(t);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] *= t[j];
-        store_chunk<WIDE>(dt + row * cols, col, cols, pack8(v));
+        store_chunk<ROWS == kActWhole>(dt + row * cols, col, cols, pack8(v));
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[j] += v[j];
@@ -713,17 +726,16 @@ void launch_rmsnorm_backward_long(const NormGradient& p, hipStream_t stream) {
                      p.dz, p.rows, p.cols, p.means, p.dx, p.partial);
 }
 
-// Groups of rows of the nonlinearity's gradient: at least four rows each, a row
-// for each wavefront; no more than the column sums take in one turn, nor than
-// fill the CUs eight times.
+// Groups of rows of the nonlinearity's gradient: whole turns; no more groups than
+// the column sums take in one turn, nor than fill the CUs eight times.
 struct RowGroups {
   int count, each;
 };
 RowGroups bias_groups(int64_t rows, int64_t cols) {
   const int64_t segments = segments_of(fp8_cols(cols) / 8, 1);
   const int64_t most = std::clamp<int64_t>(2048 / segments, 1, kSumClasses);
-  const int64_t least = rows <= 16 ? rows : (rows + most - 1) / most;
-  const int64_t each = (least + kWaves - 1) / kWaves * kWaves;
+  const int64_t turn = kWaves * kRowsAhead, least = (rows + most - 1) / most;
+  const int64_t each = (least + turn - 1) / turn * turn;
   return {static_cast<int>((rows + each - 1) / each), static_cast<int>(each)};
 }
 
@@ -745,12 +757,11 @@ void launch_activation_backward(const ActivationGradient& p, hipStream_t stream)
   const int64_t stride = fp8_cols(p.cols);
   float* sums = p.dbias == nullptr || groups.count == 1 ? p.dbias : p.workspace;
   const dim3 grid(static_cast<unsigned>(groups.count) * segments), wg(kThreads);
-  if (p.cols % 8 == 0)
-    hipLaunchKernelGGL((activation_backward_kernel<ACT, true>), grid, wg, 0, stream, p.dh, p.cq, p.cs, p.rows, p.cols,
-                       segments, groups.each, p.dt, p.dq, p.ds, sums, stride);
-  else
-    hipLaunchKernelGGL((activation_backward_kernel<ACT, false>), grid, wg, 0, stream, p.dh, p.cq, p.cs, p.rows, p.cols,
-                       segments, groups.each, p.dt, p.dq, p.ds, sums, stride);
+  const auto kernel = p.cols % 8 == 0 ? activation_backward_kernel<ACT, kActWhole>
+                    : p.cols >= 8     ? activation_backward_kernel<ACT, kActOdd>
+                                      : activation_backward_kernel<ACT, kActShort>;
+  hipLaunchKernelGGL(kernel, grid, wg, 0, stream, p.dh, p.cq, p.cs, p.rows, p.cols, segments, groups.each, p.dt, p.dq,
+                     p.ds, sums, stride);
   if (sums != p.dbias)
     hipLaunchKernelGGL(column_sums_kernel, dim3(static_cast<unsigned>((p.cols + 15) / 16)), dim3(4 * kSumClasses), 0,
                        stream, sums, groups.count, p.cols, stride, p.dbias);
