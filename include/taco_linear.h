@@ -183,11 +183,12 @@ taco_status_t taco_swiglu_backward(const void* dh_bf16, const uint8_t* cq, const
  *   TACO_ACT_GELU       t P(t), P the normal distribution function
  *   TACO_ACT_GELU_TANH  t sigmoid(2 sqrt(2 / pi) (t + 0.044715 t^3))
  *   TACO_ACT_SILU       t sigmoid(t)
- * They are taken in fp32: with w the argument of the exponential in each (t^2 / 2,
- * the sigmoid's, t), P and sigmoid have a relative error of at most
- * (4 |w| + 24) 2^-24 where they are under a half, and the same absolutely above;
- * values under 2^-100 may be 0.  A NaN stays one; at the infinities they take
- * their limits. */
+ * They are taken in fp32.  With w the argument of the exponential in each (t^2 / 2,
+ * the sigmoid's, t), P and sigmoid at -|t| have a relative error of at most
+ * (4 w + 24) 2^-24, and what is subtracted from 1 for a positive t the same
+ * absolutely; GELU's P (not its slope's) twice that, and 2^(|t| - 1) times more
+ * beyond |t| = 1, where t P(t) vanishes: 5e-6 at 0, 4e-5 at 3, 3e-3 at 8.  Values under
+ * 2^-100 may be 0.  A NaN stays one; at the infinities they take their limits. */
 enum {
   TACO_ACT_NONE = 0,
   TACO_ACT_RELU = 1,

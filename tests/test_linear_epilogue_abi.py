@@ -33,10 +33,10 @@ def test_workspace_sizes(lib):
     assert lib.taco_linear_quantize_workspace_bytes(300, 512, 8192) == lib.taco_matmul_fp8_workspace_bytes(300, 512, 8192)
     assert lib.taco_linear_quantize_workspace_bytes(0, 64, 128) == lib.taco_linear_fp8_workspace_bytes(4, 0, 128) == 0
     assert lib.taco_activation_backward_workspace_bytes(16, 4096) == 0
-    assert lib.taco_activation_backward_workspace_bytes(17, 4096) == 5 * 4096 * 4       # groups of four rows
+    assert lib.taco_activation_backward_workspace_bytes(17, 4096) == 2 * 4096 * 4       # groups of sixteen rows
     assert lib.taco_activation_backward_workspace_bytes(0, 5) == 0
     assert taco.linear_quantize_workspace_bytes(4, 64, 128) == 1024
-    assert taco.linear_fp8_workspace_bytes(4, 64, 128) == 0 and taco.activation_backward_workspace_bytes(17, 4096) == 81920
+    assert taco.linear_fp8_workspace_bytes(4, 64, 128) == 0 and taco.activation_backward_workspace_bytes(17, 4096) == 32768
 
 
 def test_linear_checks(lib):
