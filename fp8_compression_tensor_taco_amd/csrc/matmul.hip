@@ -209,6 +209,21 @@ struct SumsOut {
 // tile's rows and columns are there, and rows are 16-byte aligned; nothing branches
 // then, so that the rows' chains of instructions fill each other's gaps.
 
+// Elements [col, col + 8) of a bf16 row of n, to be settled where they are used:
+// loaded without a branch from the row's last 8 if it ends before col + 8, so that
+// nothing waits for them in between.
+__device__ __forceinline__ uint4 load_ahead(const uint16_t* row, int col, int n) {
+  uint4 u;
+  if (n >= 8) __builtin_memcpy(&u, row + min(col, n - 8), 16);
+  else u = load_chunk<false>(row, col, n);
+  return u;
+}
+__device__ __forceinline__ uint4 settled(uint4 u, int col, int n) {
+  if (n >= 8) u = drop_elements(u, min(max(col - (n - 8), 0), 7));
+  const unsigned keep = col < n ? ~0u : 0u;
+  return make_uint4(u.x & keep, u.y & keep, u.z & keep, u.w & keep);
+}
+
 // y = act(sum + bias) + residual.
 struct LinearOut {
   static constexpr bool kEpilogue = true;
@@ -216,30 +231,26 @@ struct LinearOut {
   int act;
   uint16_t* y;
   __device__ __forceinline__ bool whole_rows(int n) const { return n % 8 == 0; }
-  template <bool WHOLE, int U>
+  template <int U>
   __device__ __forceinline__ void ahead(uint4 (&more)[U], int64_t row0, int row, int apart, int left, int col, int n) const {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      more[u] = make_uint4(0, 0, 0, 0);
-      if (residual == nullptr) continue;
-      if constexpr (WHOLE)
-        more[u] = *reinterpret_cast<const uint4*>(residual + (row0 + u * apart) * n + static_cast<unsigned>(row * n + col));
-      else
-        more[u] = load_chunk<false>(residual + (row0 + min(row + u * apart, left - 1)) * n, col, n);
-    }
+    for (int u = 0; u < U; ++u)
+      if (residual != nullptr) more[u] = load_ahead(residual + (row0 + min(row + u * apart, left - 1)) * n, col, n);
   }
   template <int ACT, bool WHOLE, int U>
   __device__ __forceinline__ void finish(float (&v)[U][8], const float (&b)[8], const uint4 (&more)[U], int64_t row0,
                                          int row, int apart, int left, int col, int n) const {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float r[8];
-      unpack8(more[u], r);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[u][j] += b[j];
       activate<ACT>(v[u]);
+      if (residual != nullptr) {
+        float r[8];
+        unpack8(WHOLE ? more[u] : settled(more[u], col, n), r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[u][j] += r[j];
+        for (int j = 0; j < 8; ++j) v[u][j] += r[j];
+      }
       if constexpr (WHOLE)
         *reinterpret_cast<uint4*>(y + (row0 + u * apart) * n + static_cast<unsigned>(row * n + col)) = pack8(v[u]);
       else if (row + u * apart < left)
@@ -257,7 +268,7 @@ struct BlocksOut {
   uint8_t *hq, *hs, *cq, *cs;
   int qcols, scols;                               // of a row
   __device__ __forceinline__ bool whole_rows(int) const { return true; }
-  template <bool WHOLE, int U>
+  template <int U>
   __device__ __forceinline__ void ahead(uint4 (&)[U], int64_t, int, int, int, int, int) const {}
   template <bool WHOLE, int U>
   __device__ __forceinline__ void quantize(const float (&v)[U][8], uint8_t* q, uint8_t* scale, int64_t row0, int row,
@@ -315,34 +326,53 @@ struct SumRow {
 };
 
 // ROWS rows of sums in LDS, finished by THREADS threads: thread t takes columns
-// col of rows t / (COLS / 8) and so on.  What a turn of U rows needs from memory
-// is loaded ahead of its arithmetic.  Rows from `left` on are not there.
+// col of rows t / (COLS / 8) and so on, U rows in a turn.  What the first turn needs
+// from memory is loaded where this is made, which may be long before the sums are
+// there, and what the next one needs ahead of a turn's arithmetic.  Rows from
+// `left` on are not there.
 template <int COLS, int ROWS, int THREADS, typename Out>
-__device__ __forceinline__ void finish_rows(const Out& out, const uint8_t* lds, int thread, int row0, int left, int col0,
-                                            int n) {
-  constexpr int kPer = THREADS / (COLS / 8), kTurns = ROWS / kPer, U = kTurns < 4 ? kTurns : 4;
+struct Finish {
+  static constexpr int kPer = THREADS / (COLS / 8), kTurns = ROWS / kPer, U = kTurns < 4 ? kTurns : 4;
   static_assert(THREADS % (COLS / 8) == 0 && ROWS % kPer == 0 && kTurns % U == 0, "whole turns");
-  const int c = thread % (COLS / 8), col = col0 + 8 * c, first = thread / (COLS / 8);
-  float bias[8] = {};
-  if (out.bias != nullptr) unpack8(load_chunk<false>(out.bias, col, n), bias);
-  const auto turns = [&](auto act, auto whole) {
+  int row0, left, first, c, col, n;
+  uint4 bias, more[U];
+  __device__ __forceinline__ Finish(const Out& out, int thread, int row0_, int left_, int col0, int n_)
+      : row0(row0_), left(left_), first(thread / (COLS / 8)), c(thread % (COLS / 8)), col(col0 + 8 * c), n(n_) {
+    if (out.bias != nullptr) bias = load_ahead(out.bias, col, n);
+    out.ahead(more, row0, first, kPer, left, col, n);
+  }
+  __device__ __forceinline__ void operator()(const Out& out, const uint8_t* lds) {
+    float b[8] = {};
+    if (out.bias != nullptr) unpack8(settled(bias, col, n), b);
+    const auto turns = [&](auto act, auto whole) {
 #pragma unroll 1
-    for (int i = 0; i < kTurns; i += U) {
-      uint4 more[U];
-      float v[U][8];
-      const int row = first + i * kPer;
-      out.template ahead<whole>(more, row0, row, kPer, left, col, n);
+      for (int i = 0; i < kTurns; i += U) {
+        uint4 now[U];
+        float v[U][8];
+        const int row = first + i * kPer;
 #pragma unroll
-      for (int u = 0; u < U; ++u) SumRow<COLS>::load(lds, row + u * kPer, c, v[u]);
-      out.template finish<act, whole>(v, bias, more, row0, row, kPer, left, col, n);
-    }
-  };
-  const bool whole = left >= ROWS && col0 + COLS <= n && out.whole_rows(n);
-  with_activation(out.act, [&](auto act) {
-    if (whole) turns(act, std::true_type{});
-    else turns(act, std::false_type{});
-  });
-}
+        for (int u = 0; u < U; ++u) now[u] = more[u];
+        if (i + U < kTurns) out.ahead(more, row0, row + U * kPer, kPer, left, col, n);
+#pragma unroll
+        for (int u = 0; u < U; ++u) SumRow<COLS>::load(lds, row + u * kPer, c, v[u]);
+        out.template finish<act, whole>(v, b, now, row0, row, kPer, left, col, n);
+      }
+    };
+    const bool whole = left >= ROWS && col - 8 * c + COLS <= n && out.whole_rows(n);
+    with_activation(out.act, [&](auto act) {
+      if (whole) turns(act, std::true_type{});
+      else turns(act, std::false_type{});
+    });
+  }
+};
+template <int COLS, int ROWS, int THREADS>
+struct Finish<COLS, ROWS, THREADS, PlainOut> {
+  __device__ __forceinline__ Finish(const PlainOut&, int, int, int, int, int) {}
+};
+template <int COLS, int ROWS, int THREADS>
+struct Finish<COLS, ROWS, THREADS, SumsOut> {
+  __device__ __forceinline__ Finish(const SumsOut&, int, int, int, int, int) {}
+};
 
 // The middle sizes: tiles of BN = 16 NT WN rows of b and BM = 16 MT WM rows of
 // a.  KG groups of WN x WM wavefronts share a tile and take the steps in turn,
@@ -423,6 +453,7 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void matmul_tiles_kernel(
     copy4_to_lds(gsb + (k & ~3), 0, at + 256);
   };
 
+  Finish<T::BN, T::BM, T::kThreads, Out> finish(out, threadIdx.x, m0, m - m0, n0, n);
   const int lane_off = r * kBlock + 16 * (g ^ (r & 7));
   f32x4_t acc[NT][MT] = {};
   // scale bytes come in dwords of four steps, so a split starts at a multiple of four
@@ -498,7 +529,7 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void matmul_tiles_kernel(
           *reinterpret_cast<f32x4_t*>(rows + SumRow<T::BN>::at(16 * (MT * wm + j) + r, 4 * (NT * wn + i) + g)) = acc[i][j];
     }
     __syncthreads();
-    finish_rows<T::BN, T::BM, T::kThreads>(out, rows, threadIdx.x, m0, m - m0, n0, n);
+    finish(out, rows);
     return;
   }
   if (group == 0) {
@@ -811,11 +842,14 @@ __global__ __launch_bounds__(256) void matmul_large_kernel(
     };
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
+      const int row = m0 + 128 * wm + 64 * h, col = n0 + 128 * wn;
+      if (row >= m || col >= n) break;
+      Finish<kBlock, 64, 64, Out> finish(out, thread & 63, row, m - row, col, n);
+      fence();
       if (h == 0) hold(std::integral_constant<int, 0>{});
       else hold(std::integral_constant<int, 4>{});
       fence();
-      const int row = m0 + 128 * wm + 64 * h, col = n0 + 128 * wn;
-      if (row < m && col < n) finish_rows<kBlock, 64, 64>(out, sums, thread & 63, row, m - row, col, n);
+      finish(out, sums);
       fence();
     }
     return;
@@ -1500,10 +1534,10 @@ __global__ __launch_bounds__(256) void finish_sums_kernel(const float* __restric
   const int64_t job = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6), row = job / segments;
   if (row >= m) return;
   const int col = 8 * (64 * static_cast<int>(job - row * segments) + static_cast<int>(threadIdx.x & 63));
-  uint4 more[1] = {};
-  out.template ahead<false>(more, row, 0, 1, 1, col, n);
+  uint4 more[1] = {}, ahead = {};
+  out.ahead(more, row, 0, 1, 1, col, n);
   float bias[8] = {}, v[1][8] = {};
-  if (out.bias != nullptr) unpack8(load_chunk<false>(out.bias, col, n), bias);
+  if (out.bias != nullptr) ahead = load_ahead(out.bias, col, n);
   const float* from = sums + row * n + col;
   if (col + 8 <= n) {
 #pragma unroll 4
@@ -1519,6 +1553,7 @@ __global__ __launch_bounds__(256) void finish_sums_kernel(const float* __restric
       for (int j = 0; j < 7; ++j)
         if (col + j < n) v[0][j] += from[s * m * n + j];
   }
+  if (out.bias != nullptr) unpack8(settled(ahead, col, n), bias);
   with_activation(out.act, [&](auto act) { out.template finish<act, false>(v, bias, more, row, 0, 1, 1, col, n); });
 }
 
