@@ -69,6 +69,13 @@ __device__ __forceinline__ void copy4_to_lds(const uint8_t* base, unsigned off, 
                :: "v"(off), "s"(base), "s"(lds) : "memory", "m0");
 #endif
 }
+// The same, each lane from an address of its own.
+__device__ __forceinline__ void copy4_from_to_lds(const uint8_t* from, unsigned lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+               :: "v"(from), "s"(lds) : "memory", "m0");
+#endif
+}
 #pragma clang diagnostic pop
 
 // The tile of a workgroup.  Workgroups go to the eight XCDs in turn, so every
@@ -550,64 +557,92 @@ __global__ __launch_bounds__(64 * WN * WM * KG) void matmul_tiles_kernel(
   }
 }
 
-// Few rows of a (at most 16 MT): every byte of b is used once, so the weight's
+// All LDS reads of the wavefront are done, known to the compiler as well.
+__device__ __forceinline__ void reads_done() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0), nothing else
+  __builtin_amdgcn_sched_barrier(0);
+#endif
+}
+
+// Few rows of a (at most 8 MA): every byte of b is used once, so the weight's
 // stream from HBM is the time.  A workgroup takes 16 rows of b and its
-// wavefronts split k, each reading its fragments straight into registers, in
-// turns of kAhead steps; the partial sums are added in LDS in the wavefronts'
-// order.  No barrier but that one, no copy through LDS.  The loads of a turn are
-// not all ahead of its products: the compiler moves those of the last of the
-// four steps (MT 1), or of all but the first (MT 2), behind the first product
-// and into the branches around the others, so that a turn waits for memory
-// twice.  Kernel durations, median: 4 x 4096 x 4096: 5.5 us over weights that
-// are in the last-level cache (3.1 TB/s; launch and the two latencies are
-// most of it), 1 x 14336 x 3584: 11.6 us (4.4 TB/s), 32 x 4096 x 4096: 10.0.
+// wavefronts split k, step w, w + 8 and so on; the partial sums are added in LDS in
+// the wavefronts' order.  Each wavefront has a ring of S steps of its own in LDS
+// (16 rows of b, 8 MA of a, their scale bytes), S - 1 of them on their way: no
+// barrier but the one before the sums, and no load that the compiler would wait
+// for.  Calls over weights not in the last-level cache: 4 x 4096 x 4096 5.3 us, 4 x
+// 4096 x 16384 16.1 (4.2 TB/s), 1 x 14336 x 3584 10.8 (4.8), 32 x 4096 x 4096 6.4;
+// with the fragments loaded straight into registers, where the compiler orders and
+// waits: 5.3, 17.8, 11.9 and 9.6.  (Two such turns of loads in flight, which leaves
+// one workgroup to a CU, were slower yet: 20.5 for the second.)
 constexpr int kFewWaves = 8;
-template <int MT, typename Out>
+template <int MA, int S, typename Out>
 __global__ __launch_bounds__(64 * kFewWaves) void matmul_few_kernel(
     const uint8_t* __restrict__ qa, const uint8_t* __restrict__ sa, const uint8_t* __restrict__ qb,
     const uint8_t* __restrict__ sb, int m, int n, int kcols, int kscales, const Out out) {
-  constexpr int kAhead = 4;
-  __shared__ __align__(16) f32x4_t part[kFewWaves][MT][64];
+  constexpr int MT = (MA + 1) / 2, kA = 16 * kBlock, kScales = kA + 1024 * MA, kSlot = kScales + 256, kCopies = 3 + MA;
+  static_assert(S >= 2 && S * kSlot >= MT * 1024, "the sums fit where the rings were");
+  __shared__ __align__(128) uint8_t lds[kFewWaves * S * kSlot];
+  auto part = reinterpret_cast<f32x4_t(*)[MT][64]>(lds);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int n0 = blockIdx.x * 16, steps = kcols / kBlock;
-  const uint8_t* bp = qb + static_cast<int64_t>(min(n0 + r, n - 1)) * kcols + 16 * g;
-  const uint8_t* bs = sb + static_cast<int64_t>(n0 / kBlock) * kscales;
-  const uint8_t *ap[MT], *as[MT];
+  const int mine = (steps - wave + kFewWaves - 1) / kFewWaves;          // steps of this wavefront; may be none
+  const uint8_t* gb = uniform(qb + static_cast<int64_t>(n0) * kcols);
+  const unsigned chunk = 16 * ((lane & 7) ^ (lane >> 3));
+  unsigned off_b[2], off_a[MA];
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const int64_t row = min(16 * j + r, m - 1);
-    ap[j] = qa + row * kcols + 16 * g;
-    as[j] = sa + row * kscales;
-  }
-  auto fragment = [](const uint8_t* p) {              // chunks g and g + 4 of a row's 128 columns
-    const int4 lo = *reinterpret_cast<const int4*>(p), hi = *reinterpret_cast<const int4*>(p + 64);
-    return i32x8_t{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  for (int i = 0; i < 2; ++i) off_b[i] = static_cast<unsigned>(min(8 * i + (lane >> 3), n - 1 - n0)) * kcols + chunk;
+#pragma unroll
+  for (int i = 0; i < MA; ++i) off_a[i] = static_cast<unsigned>(min(8 * i + (lane >> 3), m - 1)) * kcols + chunk;
+  // a dword of scale bytes, four steps: of a's rows in lanes 0 to 31, of b's block in the others
+  const uint8_t* scales = lane < 32 ? sa + static_cast<int64_t>(min(lane, m - 1)) * kscales
+                                    : sb + static_cast<int64_t>(n0 / kBlock) * kscales;
+  uint8_t* ring = lds + wave * (S * kSlot);
+  const unsigned at0 = lds_address(lds) + wave * (S * kSlot);
+  auto copy_step = [&](int i, int slot) {
+    const int k = wave + kFewWaves * i;
+    const unsigned at = at0 + slot * kSlot;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) copy16_to_lds(gb + k * kBlock, off_b[c], at + 1024 * c);
+#pragma unroll
+    for (int c = 0; c < MA; ++c) copy16_to_lds(qa + k * kBlock, off_a[c], at + kA + 1024 * c);
+    copy4_from_to_lds(scales + (k & ~3), at + kScales);
   };
+  const int lane_off = r * kBlock + 16 * (g ^ (r & 7));
+  const int a_off = MA == 1 ? lane_off - (r & 8) * kBlock : lane_off;   // eight rows only: twice
   f32x4_t acc[MT] = {};
-  for (int k0 = wave; k0 < steps; k0 += kFewWaves * kAhead) {
-    i32x8_t b[kAhead], a[kAhead][MT];
-    int scale_b[kAhead], scale_a[kAhead][MT];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int k = min(k0 + u * kFewWaves, steps - 1);
-      b[u] = fragment(bp + static_cast<int64_t>(k) * kBlock);
-      scale_b[u] = bs[k];
+  for (int i = 0; i < S - 1; ++i)
+    if (i < mine) copy_step(i, i);
+  int slot = 0;
+  for (int i = 0; i < mine; ++i) {
+    if (i + S - 2 < mine)                          // step i has landed
+      copies_left<(S - 2) * kCopies>();
+    else
+      copies_left<0>();
+    const uint8_t* stage = ring + slot * kSlot;
+    const int of = (wave + kFewWaves * i) & 3;
+    i32x8_t a[MT];
+    int scale_a[MT];
+    const i32x8_t b = load_fragment(stage, lane_off);
+    const int scale_b = stage[kScales + 4 * 32 + of];
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        a[u][j] = fragment(ap[j] + static_cast<int64_t>(k) * kBlock);
-        scale_a[u][j] = as[j][k];
-      }
+    for (int j = 0; j < MT; ++j) {
+      a[j] = load_fragment(stage + kA + 16 * kBlock * j, a_off);
+      scale_a[j] = stage[kScales + 4 * (16 * j + r) + of];
     }
+    reads_done();
+    if (i + S - 1 < mine) copy_step(i + S - 1, slot == 0 ? S - 1 : slot - 1);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (k0 + u * kFewWaves < steps) {
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-          acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[u], a[u][j], acc[j], 0, 0, 0, scale_b[u], 0, scale_a[u][j]);
-      }
+    for (int j = 0; j < MT; ++j)
+      acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a[j], acc[j], 0, 0, 0, scale_b, 0, scale_a[j]);
+    slot = slot + 1 == S ? 0 : slot + 1;
   }
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < MT; ++j) part[wave][j][lane] = acc[j];
   __syncthreads();
@@ -653,15 +688,6 @@ __device__ __forceinline__ void accumulators_done(f32x4_t (&acc)[N][8]) {
     asm volatile("s_nop 15\n\ts_nop 15"
                  : "+a"(acc[i][0]), "+a"(acc[i][1]), "+a"(acc[i][2]), "+a"(acc[i][3]), "+a"(acc[i][4]),
                    "+a"(acc[i][5]), "+a"(acc[i][6]), "+a"(acc[i][7]));
-#endif
-}
-
-// All LDS reads of the wavefront are done, known to the compiler as well.
-__device__ __forceinline__ void reads_done() {
-#if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0), nothing else
-  __builtin_amdgcn_sched_barrier(0);
 #endif
 }
 
@@ -1565,9 +1591,9 @@ struct MatmulArgs {
 
 int64_t tiles_of(int64_t m, int64_t n, int64_t bm, int64_t bn) { return (m + bm - 1) / bm * ((n + bn - 1) / bn); }
 
-template <int MT, typename Out>
+template <int MA, int S, typename Out>
 void launch_few(const MatmulArgs& p, const Out& out, hipStream_t stream) {
-  hipLaunchKernelGGL((matmul_few_kernel<MT, Out>), dim3((p.n + 15) / 16), dim3(64 * kFewWaves), 0, stream, p.qa, p.sa,
+  hipLaunchKernelGGL((matmul_few_kernel<MA, S, Out>), dim3((p.n + 15) / 16), dim3(64 * kFewWaves), 0, stream, p.qa, p.sa,
                      p.qb, p.sb, p.m, p.n, p.kcols, p.kscales, out);
 }
 
@@ -1630,51 +1656,134 @@ void launch_big(const MatmulArgs& p, const Out& out, hipStream_t stream) {
 //   8192  4224  512                            44.9          29.5          37.0
 //   8192  3584  1000   99.4        56.6        50.0          37.6          33.1
 // (KG 2 of 64 x 64 has a ring of four steps and one workgroup to a CU, KG 1 a ring of
-// three and three to a CU; at 257 to 512 tiles no CU has more than two, and other
-// rings were not measured there.)
+// three and three to a CU; at 257 to 512 tiles a ring of four was no faster.)
 // so 64 x 64 tiles until a CU would have more than three, two groups of
 // wavefronts for a tile where a CU has one; 128 x 128 while their workgroups
 // are all resident (two to a CU), and 256 x 256 from there on, which loses up to
-// a quarter where few columns meet a nearly empty last round.
-// Up to 32 rows the direct loads win (16 rows: 6.7 against 9.7, 32: 9.5 against
+// a quarter where few columns meet a nearly empty last round.  (256 x 128 tiles with
+// eight wavefronts between the two were slower: 2048 x 4096 x 4096 34.7, 1021 x
+// 6400 x 1600 18.5 against 16.7.)
+// Up to 32 rows the kernel for few wins (16 rows: 5.7 against 9.7, 32: 6.4 against
 // 10.1), and at 64 rows the tiles do (15.2 against 10.5).
 //
-// Outputs in the block format need 128 columns in one workgroup: up to the 128 x
-// 128 tiles the sums go through the workspace instead, and a second kernel ends it.
+// Outputs in the block format need a block's 128 columns in one workgroup, so of the
+// smaller tiles they take 32 x 128 and 64 x 128 with two groups of wavefronts, as
+// long as every tile has a CU, and not 64 x 64 with the sums in memory and a
+// second kernel, which costs 3 to 6 us.  Measured (us, gelu, with t kept):
+//   m     n     k      32x128  64x128  128x128 KG 2  64x64, second kernel
+//   256   4096  4096   13.5    16.3    23.0          16.6
+//   64    16384 4096   14.9    17.2    23.3          17.8
+//   512   4096  4096   25.0    17.2    23.4          23.4
+//   777   1601  1600   13.8    10.0    13.4          15.0
+//   777   4096  4096   48.3    30.3    23.9          23.4
+//   128   4096  4096   12.8    15.7    22.6          12.7 (k split)
+//   300   512   8192   21.3    26.0    38.6          11.6 (k split)
+// Up to 32 rows they take the kernel for few and a second one, or, with enough
+// columns for the time of its steps on one tile to a CU, 16 x 128 tiles (us):
+//   m     n     k      16x128         few, second kernel    few (bf16 output)
+//   8     4096  4096   10.7           7.8                   5.4
+//   8     8192  4096   10.8 to 13.0   11.6 to 11.9          9.3
+//   8     16384 4096   12.6 to 17.2   17.3 to 19.2          15.2 to 17.1
+//   16    16384 4096   12.7 to 17.5   19.8 to 21.8          17.8 to 19.6
+//   32    16384 4096   12.7 to 17.5   22.0 to 25.8          20.9 to 24.8
+//   8     6400  1600   6.3            6.5                   3.8
+//   8     8192  16384  46.2           31.7                  29.1
+//   8     16384 16384  59.2           54.3                  51.6
+// (the lower figures where part of the weight is in the last-level cache), which
+// products with an epilogue and more than 8 rows take from 12288 columns on.
+enum class MatmulKernel { kFew, k64Deep, k64, k128Deep, k128, kLarge, k16Wide, k32Wide, k64Wide };
+struct MatmulPlan {
+  MatmulKernel kernel;
+  Splits splits;
+  bool sums;                                      // in the workspace, for a second kernel
+};
+enum class OutKind { kPlain, kLinear, kBlocks };
+
+MatmulPlan matmul_plan(int64_t m, int64_t n, int64_t kcols, OutKind kind) {
+  const int64_t t64 = tiles_of(m, n, 64, 64), t128 = tiles_of(m, n, 128, 128), steps = kcols / kBlock;
+  const Splits s = matmul_splits(m, n, kcols), one{1, 1 << 30};
+  if (m <= 32) {
+    if (kind == OutKind::kLinear && m > 8 && n >= 12288) return {MatmulKernel::k16Wide, one, false};
+    // 0.325 us a step on a tile, against 3 us of a second kernel and the weight at 4.5 TB/s
+    if (kind == OutKind::kBlocks && 0.325 * static_cast<double>(steps) <= 3 + static_cast<double>(n * kcols) / 4.5e6 &&
+        n * kcols <= int64_t(1) << 27)
+      return {MatmulKernel::k16Wide, one, false};
+    return {MatmulKernel::kFew, one, kind == OutKind::kBlocks};
+  }
+  if (s.count > 1) return {MatmulKernel::k64Deep, s, true};
+  if (kind == OutKind::kBlocks) {
+    if (tiles_of(m, n, 32, 128) <= 256) return {MatmulKernel::k32Wide, one, false};
+    if (tiles_of(m, n, 64, 128) <= 256) return {MatmulKernel::k64Wide, one, false};
+  } else {
+    if (t64 <= 256) return {MatmulKernel::k64Deep, one, false};
+    if (t64 <= 768) return {MatmulKernel::k64, one, false};
+  }
+  return {t128 <= 256 ? MatmulKernel::k128Deep : t128 <= 512 ? MatmulKernel::k128 : MatmulKernel::kLarge, one, false};
+}
+
+// Steps in the rings of the kernel for few rows: as many as LDS holds for one
+// workgroup to a CU, and where there are more workgroups, for two: 8 x 16384 x 4096
+// 16.2 us against 18.4.
+template <typename Out>
+void launch_few_rows(const MatmulArgs& p, const Out& out, hipStream_t stream) {
+  const bool many = p.n > 16 * 256;
+  if (p.m <= 8)
+    many ? launch_few<1, 3>(p, out, stream) : launch_few<1, 6>(p, out, stream);
+  else if (p.m <= 16)
+    many ? launch_few<2, 2>(p, out, stream) : launch_few<2, 4>(p, out, stream);
+  else
+    launch_few<4, 3>(p, out, stream);
+}
+
 template <typename Out>
 void launch_matmul(const MatmulArgs& p, const Out& out, hipStream_t stream) {
-  constexpr bool kBlocks = std::is_same_v<Out, BlocksOut>;
-  const int64_t t64 = tiles_of(p.m, p.n, 64, 64), t128 = tiles_of(p.m, p.n, 128, 128);
-  const Splits s = matmul_splits(p.m, p.n, p.kcols);
-  const auto small = [&](const auto& to) {
-    if (p.m <= 16)
-      launch_few<1>(p, to, stream);
-    else if (p.m <= 32)
-      launch_few<2>(p, to, stream);
-    else if (t64 <= 256)
-      launch_tiles<2, 2, 2, 2, 2, 4>(p, to, stream, s.count, s.steps);
+  constexpr bool kBlocks = std::is_same_v<Out, BlocksOut>, kPlain = std::is_same_v<Out, PlainOut>;
+  const MatmulPlan plan =
+      matmul_plan(p.m, p.n, p.kcols, kBlocks ? OutKind::kBlocks : kPlain ? OutKind::kPlain : OutKind::kLinear);
+  if (plan.sums) {
+    const SumsOut sums{p.workspace};
+    if (plan.kernel == MatmulKernel::kFew)
+      launch_few_rows(p, sums, stream);
     else
-      launch_tiles<2, 2, 2, 2, 1, 3>(p, to, stream);
-  };
-  if (p.m <= 32 || t64 <= 768) {
-    if (kBlocks || s.count > 1) {
-      small(SumsOut{p.workspace});
-      launch_finish(p, out, s.count, stream);
-    } else if constexpr (!kBlocks) {
-      small(out);
-    }
-  } else if (t128 <= 256)
-    launch_tiles<4, 4, 2, 2, 2, 2>(p, out, stream);
-  else if (t128 <= 512)
-    launch_tiles<4, 4, 2, 2, 1, 2>(p, out, stream);
-  else
-    launch_big(p, out, stream);
+      launch_tiles<2, 2, 2, 2, 2, 4>(p, sums, stream, plan.splits.count, plan.splits.steps);
+    launch_finish(p, out, plan.splits.count, stream);
+    return;
+  }
+  switch (plan.kernel) {
+    case MatmulKernel::kFew:
+      if constexpr (!kBlocks) launch_few_rows(p, out, stream);
+      break;
+    case MatmulKernel::k64Deep:
+      if constexpr (!kBlocks) launch_tiles<2, 2, 2, 2, 2, 4>(p, out, stream);
+      break;
+    case MatmulKernel::k64:
+      if constexpr (!kBlocks) launch_tiles<2, 2, 2, 2, 1, 3>(p, out, stream);
+      break;
+    case MatmulKernel::k128Deep:
+      launch_tiles<4, 4, 2, 2, 2, 2>(p, out, stream);
+      break;
+    case MatmulKernel::k128:
+      launch_tiles<4, 4, 2, 2, 1, 2>(p, out, stream);
+      break;
+    case MatmulKernel::kLarge:
+      launch_big(p, out, stream);
+      break;
+    case MatmulKernel::k16Wide:
+      if constexpr (!kPlain) launch_tiles<4, 1, 2, 1, 2, 4>(p, out, stream);
+      break;
+    case MatmulKernel::k32Wide:
+      if constexpr (kBlocks) launch_tiles<4, 1, 2, 2, 2, 3>(p, out, stream);
+      break;
+    case MatmulKernel::k64Wide:
+      if constexpr (kBlocks) launch_tiles<4, 2, 2, 2, 2, 3>(p, out, stream);
+      break;
+  }
 }
 
 // Bytes of sums in the workspace.
-size_t matmul_workspace(int64_t m, int64_t n, int64_t k, bool blocks) {
-  const int splits = matmul_splits(m, n, fp8_cols(k)).count;
-  return splits > 1 || (blocks && (m <= 32 || tiles_of(m, n, 64, 64) <= 768)) ? static_cast<size_t>(4 * m * n) * splits : 0;
+size_t matmul_workspace(int64_t m, int64_t n, int64_t k, OutKind kind) {
+  const MatmulPlan plan = matmul_plan(m, n, fp8_cols(k), kind);
+  return plan.sums ? static_cast<size_t>(4 * m * n) * plan.splits.count : 0;
 }
 
 template <int KT, int NT, int WK, int WN>
@@ -1769,7 +1878,7 @@ extern "C" {
 
 size_t taco_matmul_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   if (!matrix_ok(m, k) || !matrix_ok(n, k) || m > kMaxCodes / n) return 0;
-  return matmul_workspace(m, n, k, false);
+  return matmul_workspace(m, n, k, OutKind::kPlain);
 }
 
 taco_status_t taco_matmul_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb, int64_t m,
@@ -1794,7 +1903,10 @@ taco_status_t taco_matmul_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_
   return launched();
 }
 
-size_t taco_linear_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k) { return taco_matmul_fp8_workspace_bytes(m, n, k); }
+size_t taco_linear_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (!matrix_ok(m, k) || !matrix_ok(n, k) || m > kMaxCodes / n) return 0;
+  return matmul_workspace(m, n, k, OutKind::kLinear);
+}
 
 taco_status_t taco_linear_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb,
                               const void* bias_bf16, const void* residual_bf16, int32_t activation, int64_t m, int64_t n,
@@ -1824,7 +1936,7 @@ taco_status_t taco_linear_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_
 
 size_t taco_linear_quantize_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   if (!matrix_ok(m, k) || !matrix_ok(n, k) || !matrix_ok(m, n)) return 0;
-  return matmul_workspace(m, n, k, true);
+  return matmul_workspace(m, n, k, OutKind::kBlocks);
 }
 
 taco_status_t taco_linear_quantize(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb,

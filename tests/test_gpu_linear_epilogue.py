@@ -61,15 +61,19 @@ def cuda(t):
     return None if t is None else t.cuda()
 
 
-# few rows (16, 32), split, 64 x 64 with two groups and with one, 128 x 128 with two and with one, 256 x 256
-KERNELS = [(3, 300, 512), (30, 300, 512), (300, 512, 8192), (70, 300, 512), (450, 3000, 512), (1900, 1980, 512),
-           (2100, 2203, 512), (3700, 3901, 512)]
+# For quantised outputs: 16 x 128 tiles (one and two rows of them), few rows and a second kernel (up to 8, 16 and 32 rows, one
+# workgroup to a CU and two), k split, 32 x 128, 64 x 128, 128 x 128 with two groups of wavefronts and with one, 256 x 256.
+# For the others: few rows, k split, 64 x 64 with two groups and with one, 128 x 128, 256 x 256; and 16 x 128 tiles.
+KERNELS = [(3, 300, 512), (30, 300, 512), (5, 300, 2000), (12, 300, 2000), (25, 300, 2000), (300, 512, 8192), (70, 300, 512),
+           (450, 3000, 512), (1900, 1980, 512), (2100, 2203, 512), (3700, 3901, 512), (7, 4200, 1700), (14, 4200, 1700),
+           (29, 4200, 1700), (20, 12300, 300)]
+SMALLER = [s for s in KERNELS if s[0] < 3000]
 SHAPES = [(1, 1, 1), (1, 128, 128), (4, 256, 512), (3, 100, 1600), (16, 1601, 300), (17, 130, 2000), (33, 512, 4096),
           (65, 1000, 1000), (100, 257, 129), (257, 260, 1600), (777, 1601, 1600), (1, 3000, 14336), (20, 5, 8200)]
 
 
 @pytest.mark.parametrize("name", ACTS)
-@pytest.mark.parametrize("m,n,k", SHAPES + KERNELS[2:7])
+@pytest.mark.parametrize("m,n,k", SHAPES + SMALLER)
 def test_linear_fp8(m, n, k, name):
     rng = np.random.default_rng(m * n + k)
     (qa, sa), (qb, sb, _, _) = operands(rng, m, n, k)
@@ -88,7 +92,7 @@ def test_linear_fp8(m, n, k, name):
 
 
 @pytest.mark.parametrize("name", ACTS)
-@pytest.mark.parametrize("m,n,k", SHAPES + KERNELS[2:7])
+@pytest.mark.parametrize("m,n,k", SHAPES + SMALLER)
 def test_linear_quantize(m, n, k, name):
     rng = np.random.default_rng(m + n * k)
     (qa, sa), (qb, sb, _, _) = operands(rng, m, n, k)
@@ -125,6 +129,8 @@ def test_exact_sums(m, n, k):
     bias = torch.from_numpy(rng.integers(-64, 65, n) / 4).to(torch.bfloat16)
     residual = torch.from_numpy(rng.integers(-64, 65, (m, n)) / 4).to(torch.bfloat16)
     t = product + bias.float()
+    whole, out = guarded((m, n), torch.bfloat16)
+    assert torch.equal(taco.matmul_fp8(*given, out=out).cpu(), product.to(torch.bfloat16)) and survived(whole)
     for name, h in ((None, t), ("relu", t.clamp(min=0))):
         whole, out = guarded((m, n), torch.bfloat16)
         y = taco.linear_fp8(*given, bias=bias.cuda(), activation=name, residual=residual.cuda(), out=out)

@@ -75,7 +75,7 @@ def test_workspaces_of_the_callers():
               lambda w: (taco.linear_fp8(xq, xs, wq, ws, bias=bias, activation="relu", residual=residual, workspace=w),)),
              (taco.linear_quantize_workspace_bytes(300, 512, 8192),
               lambda w: taco.linear_quantize(xq, xs, wq, ws, bias=bias, activation="relu", workspace=w)),
-             (taco.linear_quantize_workspace_bytes(7, 512, 8192),
+             (taco.linear_quantize_workspace_bytes(7, 512, 8192),     # few rows, then a second kernel
               lambda w: taco.linear_quantize(xq[:7], xs[:7], wq, ws, bias=bias, activation="relu", workspace=w)),
              (taco.activation_backward_workspace_bytes(300, 512),
               lambda w: taco.activation_backward(dh, None, None, None, workspace=w))]

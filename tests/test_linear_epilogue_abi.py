@@ -27,15 +27,15 @@ def lib():
 def test_workspace_sizes(lib):
     for m, n, k in ((4, 64, 128), (300, 512, 8192), (777, 1601, 1600), (4096, 4096, 4096)):
         assert lib.taco_linear_fp8_workspace_bytes(m, n, k) == lib.taco_matmul_fp8_workspace_bytes(m, n, k)
-    assert lib.taco_linear_quantize_workspace_bytes(4, 64, 128) == 4 * 4 * 64       # the sums of small products
-    assert lib.taco_linear_quantize_workspace_bytes(777, 1601, 1600) == 4 * 777 * 1601
-    assert lib.taco_linear_quantize_workspace_bytes(4096, 4096, 4096) == 0
+    assert lib.taco_linear_quantize_workspace_bytes(4, 64, 4096) == 4 * 4 * 64      # the sums of few rows and columns
+    for m, n, k in ((4, 64, 128), (8, 16384, 4096), (777, 1601, 1600), (4096, 4096, 4096)):
+        assert lib.taco_linear_quantize_workspace_bytes(m, n, k) == 0
     assert lib.taco_linear_quantize_workspace_bytes(300, 512, 8192) == lib.taco_matmul_fp8_workspace_bytes(300, 512, 8192)
     assert lib.taco_linear_quantize_workspace_bytes(0, 64, 128) == lib.taco_linear_fp8_workspace_bytes(4, 0, 128) == 0
     assert lib.taco_activation_backward_workspace_bytes(16, 4096) == 0
     assert lib.taco_activation_backward_workspace_bytes(17, 4096) == 2 * 4096 * 4       # groups of sixteen rows
     assert lib.taco_activation_backward_workspace_bytes(0, 5) == 0
-    assert taco.linear_quantize_workspace_bytes(4, 64, 128) == 1024
+    assert taco.linear_quantize_workspace_bytes(4, 64, 4096) == 1024
     assert taco.linear_fp8_workspace_bytes(4, 64, 128) == 0 and taco.activation_backward_workspace_bytes(17, 4096) == 32768
 
 
@@ -68,7 +68,7 @@ def test_quantize_checks(lib):
     for name, p in (("qa", A + 8), ("sa", B + 1), ("qb", C + 8), ("sb", D + 2), ("bias", E + 2), ("hq", F + 8), ("hs", G + 2),
                     ("cq", H + 4), ("cs", I + 1), ("ws", W + 16)):
         assert f(**{name: p}) == ALIGN
-    assert f(ws=None, size=0) == f(size=1023) == WORKSPACE
+    assert f(k=4096, ws=None, size=0) == f(k=4096, size=1023) == WORKSPACE
     for name in ("hq", "hs", "cq", "cs", "ws"):
         for p in (A, B, C, D, E):
             assert f(**{name: p}) == ALIAS
