@@ -1,14 +1,18 @@
-"""A tensor-parallel gated MLP block's training step on the 8-bit operators, emulated on one GPU.
+"""A tensor-parallel MLP block's training step on the 8-bit operators, emulated on one GPU.
 
-    h = x + sum over ranks of down_r(silu(gate_r(norm(x))) * up_r(norm(x)))
+    gated  h = x + sum over ranks of down_r(silu(gate_r(norm(x))) * up_r(norm(x)))
+    gelu   h = x + sum over ranks of down_r(gelu(up_r(norm(x)) + b_r)) + b
 
 Each rank holds a slice of the inner width.  What is kept for the backward pass
-is in 8 bits: the norm's quantised output, the gated unit's output and its
-inputs.  The products run in FP8; the ranks' partial sums meet in the library's
+is in 8 bits: the norm's quantised output, the unit's output and its inputs.
+The products run in FP8; the ranks' partial sums meet in the library's
 compressed two-shot all-reduce, forward and backward, as they would between
-GPUs.  Master weights and their gradients are fp32, activations bf16.
+GPUs.  Master weights and their gradients are fp32, activations bf16.  The update
+is plain gradient descent, or AdamW on gradients clipped by their global norm,
+with its states in fp32 or in 8 bits.
 
-Usage: python examples/mlp_step.py [--tokens 4096] [--hidden 4096] [--inner 8192] [--ranks 2] [--steps 4]
+Usage: python examples/mlp_step.py [--mlp gated|gelu] [--optimizer sgd|adamw|adamw8] [--tokens 4096] [--hidden 4096]
+                                   [--inner 8192] [--ranks 2] [--steps 4]
 """
 from __future__ import annotations
 
@@ -32,8 +36,10 @@ class Linear:
         self.grad = torch.zeros_like(weight)
         self.quantize()
 
-    def quantize(self) -> None:
-        self.q, self.scale, self.qt, self.scale_t = taco.quantize_weight(self.weight.to(torch.bfloat16))
+    def quantize(self, copy: torch.Tensor | None = None) -> None:
+        """The 8-bit forms anew, from a bf16 copy of the weight if there is one."""
+        copy = self.weight.to(torch.bfloat16) if copy is None else copy
+        self.q, self.scale, self.qt, self.scale_t = taco.quantize_weight(copy)
 
     def forward(self, q, scale):
         return taco.matmul_fp8(q, scale, self.q, self.scale)
@@ -78,17 +84,90 @@ class MlpBlock:
         self.norm_grad += dw
         return dx
 
+    def layers(self):
+        return [*self.gate_up, *self.down]
+
+    def vectors(self):
+        """(master, gradient) of the parameters that are no matrices."""
+        return [(self.norm, self.norm_grad)]
+
     def step(self, rate: float) -> None:
         """Plain gradient descent on the master weights, then their 8-bit forms anew."""
-        self.norm -= rate * self.norm_grad
-        self.norm_grad.zero_()
-        for layer in (*self.gate_up, *self.down):
+        for master, grad in self.vectors():
+            master -= rate * grad
+            grad.zero_()
+        for layer in self.layers():
             layer.weight -= rate * layer.grad
             layer.grad.zero_()
             layer.quantize()
 
 
-def make_block(hidden: int, inner: int, ranks: int, seed: int = 0, device="cuda") -> MlpBlock:
+class GeluBlock(MlpBlock):
+    """The same with biases and GELU in the products' epilogues, and no gate."""
+
+    def __init__(self, norm: torch.Tensor, up: list[torch.Tensor], down: list[torch.Tensor], eps: float = 1e-5):
+        """norm [hidden]; per rank up [inner / ranks, hidden] and down [hidden, inner / ranks]; biases start at 0."""
+        super().__init__(norm, up, down, eps)
+        self.up_bias = [torch.zeros(w.shape[0], device=w.device) for w in up]
+        self.down_bias = torch.zeros_like(norm)
+        self.up_bias_grad = [torch.zeros_like(b) for b in self.up_bias]
+        self.down_bias_grad = torch.zeros_like(norm)
+
+    def vectors(self):
+        return [*super().vectors(), *zip(self.up_bias, self.up_bias_grad), (self.down_bias, self.down_bias_grad)]
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor):
+        z, rstd, q, scale = taco.rmsnorm_quantize(x, self.norm.to(torch.bfloat16), self.eps, residual=residual)
+        self.kept = [z, rstd, q, scale]
+        partial = []
+        for r, (up, down, bias) in enumerate(zip(self.gate_up, self.down, self.up_bias)):
+            kept = taco.linear_quantize(q, scale, up.q, up.scale, bias=bias.to(torch.bfloat16), activation="gelu")
+            self.kept.append(kept)
+            partial.append(taco.linear_fp8(kept[0], kept[1], down.q, down.scale,
+                                           bias=self.down_bias.to(torch.bfloat16) if r == 0 else None))
+        return self._sum(partial), z
+
+    def backward(self, dy: torch.Tensor, dz: torch.Tensor) -> torch.Tensor:
+        z, rstd, q, scale, *ranks = self.kept
+        _, dq, ds, dbias = taco.activation_backward(dy, None, None, None)
+        self.down_bias_grad += dbias
+        partial = []
+        for up, down, (hq, hs, cq, cs), grad in zip(self.gate_up, self.down, ranks, self.up_bias_grad):
+            dh = down.backward(dy, dq, ds, hq, hs)
+            dt, tq, ts, dbias = taco.activation_backward(dh, cq, cs, "gelu")
+            grad += dbias
+            partial.append(up.backward(dt, tq, ts, q, scale))
+        dx, dw = taco.rmsnorm_backward(self._sum(partial), z, rstd, self.norm.to(torch.bfloat16), dz=dz)
+        self.norm_grad += dw
+        return dx
+
+
+class AdamW:
+    """A block's update: one norm and one step for all parameters; matrices' states in `bits`, the others' in fp32."""
+
+    def __init__(self, block: MlpBlock, rate: float, bits: int = 32, max_norm: float = 1.0, weight_decay: float = 0.01):
+        self.block, self.rate, self.max_norm, self.weight_decay, self.steps = block, rate, max_norm, weight_decay, 0
+        self.params = [layer.weight for layer in block.layers()] + [p for p, _ in block.vectors()]
+        matrices = len(block.layers())
+        states = [taco.adamw_state(p, bits if i < matrices else 32) for i, p in enumerate(self.params)]
+        self.m, self.v = ([s[k] for s in states] for k in (0, 1))
+        self.copies = [torch.empty_like(p, dtype=torch.bfloat16) if i < matrices else None for i, p in enumerate(self.params)]
+
+    def step(self) -> torch.Tensor:
+        """Returns the gradients' norm and the factor that clipped it."""
+        grads = [layer.grad for layer in self.block.layers()] + [g for _, g in self.block.vectors()]
+        self.steps += 1
+        norm = taco.gradient_norm(grads, self.max_norm)
+        taco.adamw_step(self.params, grads, self.m, self.v, lr=self.rate, step=self.steps, weight_decay=self.weight_decay,
+                        grad_scale=norm[1:], copies=self.copies, seed=self.steps)
+        for layer, copy in zip(self.block.layers(), self.copies):
+            layer.quantize(copy)
+        for grad in grads:
+            grad.zero_()
+        return norm
+
+
+def make_block(hidden: int, inner: int, ranks: int, seed: int = 0, device="cuda", mlp: str = "gated") -> MlpBlock:
     if inner % ranks:
         raise ValueError("the inner width must split evenly over the ranks")
     g = torch.Generator(device=device).manual_seed(seed)
@@ -97,8 +176,9 @@ def make_block(hidden: int, inner: int, ranks: int, seed: int = 0, device="cuda"
     def weight(rows, cols, fan):
         return torch.randn(rows, cols, device=device, generator=g) * fan ** -0.5
 
-    return MlpBlock(torch.ones(hidden, device=device), [weight(2 * width, hidden, hidden) for _ in range(ranks)],
-                    [weight(hidden, width, inner) for _ in range(ranks)])
+    kind, rows = (MlpBlock, 2 * width) if mlp == "gated" else (GeluBlock, width)
+    return kind(torch.ones(hidden, device=device), [weight(rows, hidden, hidden) for _ in range(ranks)],
+                [weight(hidden, width, inner) for _ in range(ranks)])
 
 
 def main() -> None:
@@ -108,8 +188,11 @@ def main() -> None:
     a.add_argument("--inner", type=int, default=8192)
     a.add_argument("--ranks", type=int, default=2)
     a.add_argument("--steps", type=int, default=4)
+    a.add_argument("--mlp", choices=("gated", "gelu"), default="gated")
+    a.add_argument("--optimizer", choices=("sgd", "adamw", "adamw8"), default="sgd")
     args = a.parse_args()
-    block = make_block(args.hidden, args.inner, args.ranks)
+    block = make_block(args.hidden, args.inner, args.ranks, mlp=args.mlp)
+    adamw = None if args.optimizer == "sgd" else AdamW(block, 1e-4, 8 if args.optimizer == "adamw8" else 32)
     g = torch.Generator(device="cuda").manual_seed(1)
 
     def draw():
@@ -122,7 +205,10 @@ def main() -> None:
         y, z = block.forward(x, residual)
         error = y.float() - target.float()
         block.backward((error * (2 / error.numel())).to(torch.bfloat16), torch.zeros_like(z))
-        block.step(0.05 * args.hidden)
+        if adamw is None:
+            block.step(0.05 * args.hidden)
+        else:
+            adamw.step()
         end.record()
         torch.cuda.synchronize()
         print(f"step {k}: loss {float(error.square().mean()):.5f}, {begin.elapsed_time(end):.3f} ms", flush=True)
