@@ -29,17 +29,18 @@ def philox(counter, key, rounds=7):
     return np.stack(x, 1)
 
 
-def random_halves(n, index, step, seed):
-    """16 bits of each element for m, for sqrt(v) and for a bf16 parameter."""
-    e = np.arange(n)
+def random_halves(n, index, step, seed, first=0):
+    """16 bits of each element, from `first` on, for m, for sqrt(v) and for a bf16 parameter."""
+    at = np.arange(n)
+    e = at + first
     key = (seed & 0xFFFFFFFF, seed >> 32)
 
     def words(call):
         c = np.stack([e // 8, call, np.full(n, index), np.full(n, step & 0xFFFFFFFF)], 1)
         return philox(c, key)
 
-    w = words(e % 8 // 4)[e, e % 4].astype(np.int64)
-    p = words(np.full(n, 2))[e, e % 8 // 2].astype(np.int64)
+    w = words(e % 8 // 4)[at, e % 4].astype(np.int64)
+    p = words(np.full(n, 2))[at, e % 8 // 2].astype(np.int64)
     return w & 0xFFFF, w >> 16, np.where(e % 2 == 0, p & 0xFFFF, p >> 16)
 
 
@@ -72,13 +73,13 @@ def decode_state(state, n):
     return (e4m3_decode(q) * np.repeat(ol.scale_values(s[:len(q) // 128]), 128))[:n]
 
 
-def adamw(p, grad, m, v, *, lr, step, betas, eps, decay, factor=1.0, index=0, seed=0, bf16=False):
-    """(p', m', v') of one tensor; m, v fp32 arrays or pairs of codes and scale bytes (then pairs come back).
+def adamw(p, grad, m, v, *, lr, step, betas, eps, decay, factor=1.0, index=0, seed=0, bf16=False, first=0):
+    """(p', m', v') of one tensor, or of its elements from `first` on, a multiple of 128; m, v fp32 arrays or pairs of codes and scale bytes (then pairs come back).
 
     p' in fp64, with the stochastic rounding for bf16."""
     n = len(p)
     bits8 = isinstance(m, tuple)
-    half_m, half_v, half_p = random_halves(n, index, step, seed)
+    half_m, half_v, half_p = random_halves(n, index, step, seed, first)
     g = np.asarray(grad, F) * F(factor)
     m_, r_ = (decode_state(m, n).astype(F), decode_state(v, n).astype(F)) if bits8 else (np.asarray(m, F), None)
     v_ = r_ * r_ if bits8 else np.asarray(v, F)

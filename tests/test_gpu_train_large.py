@@ -1,0 +1,95 @@
+"""Past 2^32 elements: the product's epilogues, the nonlinearity's gradient and the training step's update, on slices
+around the borders that 32-bit offsets would wrap at.
+
+The products' operands are 0, 1, 1.5 and 2 with scales 1 and 2, whose sums are exact whichever kernel makes them, so a call
+on a few of the rows gives the same values bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_compression_tensor_taco_amd as taco
+from oracle import linear as ol
+from oracle import optim as oo
+from test_gpu_linear import f64
+from test_gpu_optim import check_parameter
+
+pytestmark = pytest.mark.gpu
+
+
+def small_codes(rows, cols, seed):
+    values = torch.tensor([0x00, 0x38, 0x3C, 0x40, 0xB8, 0xBC, 0xC0], dtype=torch.uint8, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return values[torch.randint(0, 7, (rows, cols), device="cuda", generator=gen)]
+
+
+def test_epilogues_and_gradient():
+    m, n = 66000, 65600                                        # 4.33e9 elements; the last tiles are partial both ways
+    qa, qb = small_codes(m, 128, 0), small_codes(n, 128, 1)
+    sa = torch.full((m, 4), 127, dtype=torch.uint8, device="cuda")
+    sb = torch.full((-(-n // 128), 4), 128, dtype=torch.uint8, device="cuda")
+    bias = (torch.arange(n, device="cuda") % 64 / 4).to(torch.bfloat16)
+    border = 2 ** 32 // n
+    rows = torch.tensor([0, 1, border // 2, border - 1, border, border + 1, 2 ** 31 // n, m - 2, m - 1], device="cuda")
+    y = taco.linear_fp8(qa, sa, qb, sb, bias=bias, activation="gelu")
+    few = taco.linear_fp8(qa[rows], sa[rows], qb, sb, bias=bias, activation="gelu")
+    assert torch.equal(y[rows], few)
+    z = taco.linear_fp8(qa, sa, qb, sb, bias=bias, residual=y)
+    assert torch.equal(z[rows], taco.linear_fp8(qa[rows], sa[rows], qb, sb, bias=bias, residual=few))
+    del z
+    hq, hs, cq, cs = taco.linear_quantize(qa, sa, qb, sb, bias=bias, activation="gelu")
+    got = taco.linear_quantize(qa[rows], sa[rows], qb, sb, bias=bias, activation="gelu")
+    assert all(torch.equal(a[rows], b) for a, b in zip((hq, hs, cq, cs), got))
+    del hq, hs
+    dt, dq, ds, dbias = taco.activation_backward(y, cq, cs, "gelu")
+    part = taco.activation_backward(few, cq[rows], cs[rows], "gelu")
+    assert all(torch.equal(a[rows], b) for a, b in zip((dt, dq, ds), part))
+    # columns' sums: within (rows + 64) roundings of the terms' magnitudes, dt's own rounding to bf16 besides
+    for c in (0, 1, 40000, n - 1):
+        terms = dt[:, c].double()
+        assert abs(float(dbias[c]) - float(terms.sum())) <= ((m + 64) * 2.0 ** -24 + 2.0 ** -8) * float(terms.abs().sum())
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_update(bits):
+    n, hyper = 2 ** 32 + 3000 + 77, dict(lr=3e-3, step=7, betas=(0.9, 0.99), eps=1e-8)
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    piece = torch.randn(1 << 20, device="cuda", generator=gen)
+
+    def filled(dtype, scale):
+        x = torch.empty(n, dtype=dtype, device="cuda")
+        for at in range(0, n, 1 << 20):
+            part = x[at:at + (1 << 20)]
+            part.copy_(piece[:part.numel()] * (scale * (1 + at / n)))
+        return x
+
+    p, g = filled(torch.bfloat16, 0.02), filled(torch.bfloat16, 1e-3)
+    if bits == 8:
+        m, v = taco.adamw_state(p, 8)
+        m[0].random_(0x20, 0x70, generator=gen)
+        v[0].random_(0x20, 0x70, generator=gen)
+        m[0][n:], v[0][n:] = 0, 0
+        m[1][:-(-n // 128)].fill_(110)
+        v[1][:-(-n // 128)].fill_(110)
+    else:
+        m, v = torch.full((n,), 1e-3, device="cuda"), torch.full((n,), 1e-6, device="cuda")
+    slices = [(s, min(s + 1024, n)) for s in (0, 2 ** 31 - 512, 2 ** 32 - 512, 2 ** 32, n - n % 128 - 896)]
+
+    def part(state, a, b):
+        if not isinstance(state, tuple):
+            return state[a:b].cpu().numpy()
+        return state[0][a:-(-b // 128) * 128].cpu().numpy(), state[1][a // 128:-(-b // 128)].cpu().numpy()
+
+    before = [(f64(p[a:b]), f64(g[a:b]), part(m, a, b), part(v, a, b)) for a, b in slices]
+    norm = taco.gradient_norm([g])
+    taco.adamw_step([p], [g], [m], [v], weight_decay=0.1, seed=5, **hyper)
+    total = sum(float(g[at:at + (1 << 28)].double().square().sum()) for at in range(0, n, 1 << 28)) ** 0.5
+    assert abs(float(norm[0]) - total) <= 1e-6 * total
+    for (a, b), (p0, g0, m0, v0) in zip(slices, before):
+        new, want_m, want_v = oo.adamw(p0, g0, m0, v0, decay=0.1, seed=5, first=a, **hyper)
+        for got, want in ((m, want_m), (v, want_v)):
+            got = part(got, a, b)
+            if bits == 8:
+                assert (got[0] == want[0]).all() and (got[1] == want[1][:len(got[1])]).all()
+            else:
+                assert (got == want).all()
+        check_parameter(p[a:b], new, p0, hyper["lr"], 0.1, oo.random_halves(b - a, 0, hyper["step"], 5, a)[2])
