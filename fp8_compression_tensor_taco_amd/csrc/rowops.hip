@@ -726,15 +726,17 @@ void launch_rmsnorm_backward_long(const NormGradient& p, hipStream_t stream) {
                      p.dz, p.rows, p.cols, p.means, p.dx, p.partial);
 }
 
-// Groups of rows of the nonlinearity's gradient: whole turns; no more groups than
-// the column sums take in one turn, nor than fill the CUs eight times.
+// Groups of rows of the nonlinearity's gradient, whole turns each: about four
+// workgroups to a CU, and more where a group would have more than 64 rows; no more
+// groups than the column sums take in one turn.  With 512, 1024, 2048 and 4096
+// workgroups at most: 4096 x 4096 without a nonlinearity 18.6, 14.7, 15.8 and 15.8
+// us, 8192 x 14336 180, 160, 162 and 152.
 struct RowGroups {
   int count, each;
 };
 RowGroups bias_groups(int64_t rows, int64_t cols) {
-  const int64_t segments = segments_of(fp8_cols(cols) / 8, 1);
-  const int64_t most = std::clamp<int64_t>(2048 / segments, 1, kSumClasses);
-  const int64_t turn = kWaves * kRowsAhead, least = (rows + most - 1) / most;
+  const int64_t segments = segments_of(fp8_cols(cols) / 8, 1), turn = kWaves * kRowsAhead;
+  const int64_t least = std::max(std::min<int64_t>((rows * segments + 1023) / 1024, 64), (rows + kSumClasses - 1) / kSumClasses);
   const int64_t each = (least + turn - 1) / turn * turn;
   return {static_cast<int>((rows + each - 1) / each), static_cast<int>(each)};
 }
