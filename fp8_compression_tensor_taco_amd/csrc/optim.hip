@@ -267,7 +267,13 @@ __device__ __forceinline__ void adamw_tile(const AdamwArgs& o, const AdamwTensor
   }
 }
 
-// One pass: a workgroup takes kAdamwTile elements of one tensor.
+// One pass: a workgroup takes kAdamwTile elements of one tensor.  Four elements a
+// lane and load, so that every access of a wavefront is consecutive, and two such
+// sets for loads in flight.  30.7M elements with fp32 states and a copy: 151 us, 6.1
+// TB/s, part of it from the last-level cache; 201M with 8-bit states and a copy: 665
+// us, 5.4 TB/s.  48 tensors of 1600 to 6400 elements: 5.6 us, the latencies of finding
+// the tensor, its descriptor, the elements and the stores in turn (one tensor of as
+// many: 4.0).
 template <bool BITS8>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwArgs o) {
   const int i = find_tensor(o.first, o.tensors, blockIdx.x);
@@ -317,9 +323,10 @@ __device__ __forceinline__ double group_sum(double v) {       // in a fixed orde
   return v;
 }
 
-// A workgroup takes tiles gridDim.x apart and writes its sum of squares.  30.7M
-// fp32 elements 22 us, 201M 129 (6.2 TB/s, part of it from the last-level cache),
-// 201M bf16 NNN; behind a step that has just written as much, 39 for the first.
+// A workgroup takes tiles gridDim.x apart and writes its sum of squares.  With the
+// sum of those: 30.7M fp32 elements 22 us, 201M 134 (6.0 TB/s, part of it from the
+// last-level cache), 201M bf16 71; 30.7M behind a step that has just written eight
+// times as much, 39.  48 tensors of 1600 to 6400 elements: 3.6 us and 1.9, latency.
 __global__ __launch_bounds__(kThreads) void square_sums_kernel(const NormArgs o, double* __restrict__ sums) {
   double acc[4] = {};
   const auto add = [&](float v, int j) { acc[j] = fma(static_cast<double>(v), static_cast<double>(v), acc[j]); };

@@ -588,7 +588,10 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_any_kernel(
 // `each` rows, a wavefront every fourth of them, kRowsAhead at a time so that
 // their loads are under way together; a lane keeps its 8 columns' sums in
 // registers, the wavefronts' are added in LDS in order, and the workgroup writes
-// one row of `sums` (dbias itself where there is but one group of rows).
+// one row of `sums` (dbias itself where there is but one group of rows), which
+// column_sums_kernel adds.  4096 x 16384 with gelu: 85 us, 4.7 TB/s, and 5 for the
+// sums; 4096 x 4096 without a nonlinearity: 12 and 3; 1021 x 1601 with silu: 6.5 and 3,
+// latency.
 //
 // The loads have no branch, so that the compiler can count them and waits for one
 // row while the next ones' are under way: lanes past the end of a row load its last
