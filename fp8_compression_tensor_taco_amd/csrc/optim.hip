@@ -474,10 +474,12 @@ void launch_adamw(AdamwArgs& args, unsigned blocks, hipStream_t stream) {
 }
 
 // The tensors with 8-bit states, or the others, in launches of up to
-// kAdamwTensors and 2^31 workgroups.
+// kAdamwTensors and 2^31 threads (a launch has fewer than 2^32); the largest
+// tensor has as many.
 template <bool BITS8>
 bool launch_all(AdamwArgs& args, const taco_adamw_tensor_t* tensors, int64_t count, hipStream_t stream) {
-  constexpr int64_t kMost = int64_t(1) << 30;
+  constexpr int64_t kMost = (int64_t(1) << 31) / kThreads;
+  static_assert(kMaxCodes <= kMost * kAdamwTile, "a tensor fits a launch");
   int64_t blocks = 0;
   for (int64_t i = 0; i < count; ++i) {
     const taco_adamw_tensor_t& t = tensors[i];

@@ -93,3 +93,27 @@ def test_update(bits):
             else:
                 assert (got == want).all()
         check_parameter(p[a:b], new, p0, hyper["lr"], 0.1, oo.random_halves(b - a, 0, hyper["step"], 5, a)[2])
+
+
+def test_update_of_more_threads_than_a_launch_has():
+    """Tensors of the largest size with 8-bit states, whose workgroups of 2048 elements have 2^32 threads, and a short one
+    behind them.  Gradients are shared, which is allowed: they are only read."""
+    sizes, hyper = [2 ** 34, 2 ** 34, 1000], dict(lr=1e-2, step=1, betas=(0.9, 0.99), eps=1e-8)
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 180 << 30:
+        pytest.skip("needs 161 GiB")
+    g = torch.full((2 ** 34,), 0.5, dtype=torch.bfloat16, device="cuda")
+    params = [torch.zeros(n, dtype=torch.bfloat16, device="cuda") for n in sizes]
+    states = [taco.adamw_state(p, 8) for p in params]
+    taco.adamw_step(params, [g[:n] for n in sizes], [m for m, _ in states], [v for _, v in states], weight_decay=0.0, seed=3,
+                    **hyper)
+    for i, (n, p, (m, v)) in enumerate(zip(sizes, params, states)):
+        for a in {0, n // 2 // 128 * 128, (n - 1) // 128 * 128 - 256}:
+            b = min(a + 384, n)
+            zeros = np.zeros(-(-b // 128) * 128 - a, np.uint8), np.full(-(-b // 128) - a // 128, 127, np.uint8)
+            new, *want = oo.adamw(np.zeros(b - a), np.full(b - a, 0.5, np.float32), zeros, zeros, decay=0.0, index=i, seed=3,
+                                  first=a, **hyper)
+            for (q, s), (wq, ws) in zip((m, v), want):
+                assert (q[a:a + len(zeros[0])].cpu().numpy() == wq).all()
+                assert (s[a // 128:a // 128 + len(zeros[1])].cpu().numpy() == ws[:len(zeros[1])]).all()
+            check_parameter(p[a:b], new, np.zeros(b - a), hyper["lr"], 0.0, oo.random_halves(b - a, i, 1, 3, a)[2])
