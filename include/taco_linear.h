@@ -218,6 +218,8 @@ taco_status_t taco_linear_fp8(const uint8_t* qa, const uint8_t* sa, const uint8_
  *   hq, hs  out: h [m, n] in the block format
  *   cq, cs  out: t [m, n] in the block format, the checkpoint that
  *           taco_activation_backward takes.  Both NULL: not kept.
+ * A block whose largest value is nearer to the border of two scales than the sums'
+ * error may take either; its values are then coded as that scale's.
  * h and t within the limits above (TACO_ERR_SHAPE).
  */
 size_t taco_linear_quantize_workspace_bytes(int64_t m, int64_t n, int64_t k);
